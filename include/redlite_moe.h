@@ -83,8 +83,14 @@ enum {
 enum {
   REDLITE_STATUS_BAD_ID = 1,     /* an expert id outside [0, n_experts) */
   REDLITE_STATUS_BAD_EXPERT = 2, /* selected slot has null matrices, bad qtype or shape */
-  REDLITE_STATUS_TIMEOUT = 4     /* a bounded in-kernel wait gave up */
+  REDLITE_STATUS_TIMEOUT = 4,    /* a bounded in-kernel wait gave up */
+  REDLITE_STATUS_BAD_LENGTH = 8, /* a sequence length, start or offset the buffers cannot hold */
+  REDLITE_STATUS_BAD_PAGE = 16,  /* a block-table entry outside [0, n_pages) where a page is needed */
+  REDLITE_STATUS_BAD_SLOT = 32   /* a state slot outside [0, n_slots), or named twice in one call */
 };
+
+/* Element types of the token mixers' activations. */
+typedef enum { REDLITE_T_F32 = 0, REDLITE_T_BF16 = 1, REDLITE_T_F16 = 2 } redlite_dtype;
 
 /* One expert slot.  gate/up/down are device pointers to packed matrices. */
 typedef struct {
@@ -334,6 +340,79 @@ size_t redlite_proj_matrix_bytes(int32_t qtype, int64_t rows, int64_t k);
  * REDLITE_EUNSUPPORTED if k is not a multiple of 256; enqueued on stream. */
 int redlite_proj_gemv(int32_t qtype, const void *W, int64_t rows, int64_t k, const float *x, int32_t n_tokens,
                       float *y, void *stream);
+
+/* ------------------------------------------------------------- token mixers
+ * The operators between the projections and the block above, for the two
+ * kinds of layer of the model the pages run ("Red Lite dev16", section
+ * "Pinned full-attention graph": grouped-query attention over a K/V cache;
+ * "Red Lite dev15", section "Field-derived recurrent dimensions": the
+ * DeltaNet state update).  Common to all of them:
+ *   - dtype (redlite_dtype) is the element type of the activations in and
+ *     out; sums, softmax statistics and states are fp32.
+ *   - Activations are rows of heads: element (token, head, i) of x lies at
+ *     x + token * x_stride + head * head_dim + i, x_stride in elements, at
+ *     least heads * head_dim, rows and bases on 16-byte boundaries (so q, k
+ *     and v may be slices of one joint projection).  Outputs must not
+ *     overlap inputs except where stated.
+ *   - Sequences are packed: cu is a device array [n_seqs + 1] of ascending
+ *     offsets; sequence s holds rows cu[s] .. cu[s + 1] - 1 (possibly none)
+ *     of the n_tokens rows.  Rows in front of cu[0] or behind cu[n_seqs] are
+ *     neither read nor written.
+ *   - status: a device word into which REDLITE_STATUS_* bits are ORed, or
+ *     NULL.  Lengths, pages and slots are checked on the device before they
+ *     are used; what cannot be served is reported and skipped.
+ *   - No call keeps anything between calls.  A workspace holds nothing that
+ *     a later call needs, needs no initialisation, and must not be used by
+ *     two calls that may run at the same time.
+ *   - n_tokens = 0 (or n_seqs = 0) returns REDLITE_OK and enqueues nothing.
+ *   - REDLITE_EINVAL: a null pointer, a size, stride or alignment out of
+ *     range; REDLITE_EUNSUPPORTED: a head size or page size the kernels do
+ *     not take; REDLITE_ENOMEM: workspace too small. */
+
+/* The paged key/value cache in 4 bits.  A page holds page_size tokens (a
+ * multiple of 16, up to 4096) of all key/value heads, redlite_kv4_page_bytes
+ * bytes; a cache is n_pages of them, 16-byte aligned (one cache per layer).
+ * block_table: device int32 [n_seqs, max_pages], entry p the page of tokens
+ * p * page_size .. of a sequence (entries of pages that are not reached are
+ * not read; a page may serve several sequences as long as none writes it).
+ * Values are kept in groups of 32 along the head:
+ *   m = fp16(min), d = fp16((max - m) / 15) (difference and quotient in
+ *   fp32), code = the nearest of 0..15 to (x - m) / d (ties to even, 0 if
+ *   d = 0); the cache stands for m + d * code.
+ * Inputs are clamped to +-65504; a group that holds a NaN or an infinity
+ * reads back as NaN.  head_dim 128 or 256. */
+size_t redlite_kv4_page_bytes(int32_t n_kv_heads, int32_t head_dim, int32_t page_size);
+
+/* Store the new tokens' keys and values: row cu[s] + i of k and v becomes
+ * token start[s] + i of sequence s.  start: device int32 [n_seqs].  Of two
+ * rows that a call maps to one place, one is stored (which one is open). */
+int redlite_kv4_append(int32_t dtype, const void *k, const void *v, int64_t k_stride, int64_t v_stride,
+                       const int32_t *cu_tokens, const int32_t *start, int32_t n_seqs, int32_t n_tokens,
+                       int32_t n_kv_heads, int32_t head_dim, int32_t page_size, const int32_t *block_table,
+                       int32_t max_pages, int64_t n_pages, void *cache, int32_t *status, void *stream);
+
+/* The reverse: rows of k and v become the values the cache stands for
+ * (rounded to dtype); a row whose page is missing becomes zeros (reported). */
+int redlite_kv4_load(int32_t dtype, const void *cache, int32_t n_kv_heads, int32_t head_dim, int32_t page_size,
+                     const int32_t *block_table, int32_t max_pages, int64_t n_pages, const int32_t *cu_tokens,
+                     const int32_t *start, int32_t n_seqs, int32_t n_tokens, void *k, void *v, int64_t k_stride,
+                     int64_t v_stride, int32_t *status, void *stream);
+
+/* Attention of one query per sequence over its cached tokens:
+ *   out[s, h] = sum_{t < lens[s]} softmax_t(scale * q[s, h] . K[t, kh]) V[t, kh]
+ * K, V the values the cache stands for, used unrounded.  lens: device int32
+ * [n_seqs]; a sequence of length 0 gives zeros, and so does one whose length
+ * is negative or beyond max_pages * page_size (reported); tokens on a page
+ * that is not in the cache are left out (reported).
+ *   q, out   device [n_seqs rows, n_heads * head_dim]
+ *   workspace device, 16-byte aligned, redlite_kv4_decode_workspace_bytes()
+ * The result does not depend on the order in which blocks run. */
+size_t redlite_kv4_decode_workspace_bytes(int32_t n_seqs, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim);
+int redlite_kv4_decode(int32_t dtype, const void *q, int64_t q_stride, int32_t n_seqs, int32_t n_heads,
+                       int32_t n_kv_heads, int32_t head_dim, const void *cache, int32_t page_size,
+                       const int32_t *block_table, int32_t max_pages, int64_t n_pages, const int32_t *lens, float scale,
+                       void *out, int64_t out_stride, void *workspace, size_t workspace_bytes, int32_t *status,
+                       void *stream);
 
 /* ---------------------------------------------------------------- slot pool
  * The bounded, top-k-aware LRU pool of expert slots ("Red Metal dev8",

@@ -28,8 +28,16 @@ REDLITE_EAGAIN = -5
 REDLITE_STATUS_BAD_ID = 1
 REDLITE_STATUS_BAD_EXPERT = 2
 REDLITE_STATUS_TIMEOUT = 4
+REDLITE_STATUS_BAD_LENGTH = 8
+REDLITE_STATUS_BAD_PAGE = 16
+REDLITE_STATUS_BAD_SLOT = 32
+REDLITE_T_F32 = 0
+REDLITE_T_BF16 = 1
+REDLITE_T_F16 = 2
 
 _c_void_p = ctypes.c_void_p
+_i32 = ctypes.c_int32
+_i64 = ctypes.c_int64
 
 
 class redlite_moe_expert(ctypes.Structure):
@@ -92,6 +100,15 @@ EXPORTS = {
     "redlite_proj_matrix_bytes": (ctypes.c_size_t, [ctypes.c_int32, ctypes.c_int64, ctypes.c_int64]),
     "redlite_proj_gemv": (ctypes.c_int, [ctypes.c_int32, _c_void_p, ctypes.c_int64, ctypes.c_int64, _c_void_p,
                                          ctypes.c_int32, _c_void_p, _c_void_p]),
+    "redlite_kv4_page_bytes": (ctypes.c_size_t, [_i32] * 3),
+    "redlite_kv4_append": (ctypes.c_int, [_i32, _c_void_p, _c_void_p, _i64, _i64, _c_void_p, _c_void_p, _i32, _i32, _i32,
+                                          _i32, _i32, _c_void_p, _i32, _i64, _c_void_p, _c_void_p, _c_void_p]),
+    "redlite_kv4_load": (ctypes.c_int, [_i32, _c_void_p, _i32, _i32, _i32, _c_void_p, _i32, _i64, _c_void_p, _c_void_p,
+                                        _i32, _i32, _c_void_p, _c_void_p, _i64, _i64, _c_void_p, _c_void_p]),
+    "redlite_kv4_decode_workspace_bytes": (ctypes.c_size_t, [_i32] * 4),
+    "redlite_kv4_decode": (ctypes.c_int, [_i32, _c_void_p, _i64, _i32, _i32, _i32, _i32, _c_void_p, _i32, _c_void_p,
+                                          _i32, _i64, _c_void_p, ctypes.c_float, _c_void_p, _i64, _c_void_p,
+                                          ctypes.c_size_t, _c_void_p, _c_void_p]),
     "redlite_moe_pack_matrix": (ctypes.c_int, [ctypes.c_int32, ctypes.c_int64, ctypes.c_int64, _c_void_p,
                                                _c_void_p]),
     "redlite_moe_dequant": (ctypes.c_int, [ctypes.c_int32, _c_void_p, ctypes.c_int64, ctypes.c_int64, _c_void_p,
@@ -267,6 +284,121 @@ def redlite_proj_gemv(qtype: int, W: torch.Tensor, rows: int, k: int, x: torch.T
                       y: torch.Tensor, stream=None) -> int:
     """y = W x for a Q8_0-style (3) or Q4_K-style (4) projection matrix."""
     return lib().redlite_proj_gemv(qtype, _ptr(W), rows, k, _ptr(x), n_tokens, _ptr(y), _stream_handle(stream))
+
+
+# ---------------------------------------------------------------- token mixers
+# Activations are [rows, heads, head_dim] tensors whose rows may be strided
+# (slices of a joint projection); sizes and the element type are read off the
+# tensors.  A call runs on the tensors' device, on `stream` or that device's
+# current stream; `status` is an optional int32 tensor of one element.
+
+_DTYPES = {torch.float32: REDLITE_T_F32, torch.bfloat16: REDLITE_T_BF16, torch.float16: REDLITE_T_F16}
+
+
+def _heads_ok(t: torch.Tensor) -> bool:
+    """[rows, heads, head_dim] on a GPU with dense heads; only the row stride is free."""
+    return (t.is_cuda and t.dim() == 3 and t.dtype in _DTYPES and (t.shape[2] <= 1 or t.stride(2) == 1)
+            and (t.shape[1] <= 1 or t.stride(1) == t.shape[2]))
+
+
+def _row_stride(t: torch.Tensor) -> int:
+    # the stride of a dimension of one element says nothing
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def _dense(t: Optional[torch.Tensor], dtype: torch.dtype, device) -> bool:
+    return t is None or (t.dtype == dtype and t.is_contiguous() and t.device == device)
+
+
+def _mixer_ok(acts, dense) -> bool:
+    """Activations of one type and device; (tensor, dtype) pairs that are dense and beside them."""
+    d, t = acts[0].device, acts[0].dtype
+    return (all(_heads_ok(x) and x.device == d and x.dtype == t for x in acts)
+            and all(_dense(x, dt, d) for x, dt in dense))
+
+
+def _on(device, stream):
+    s = torch.cuda.current_stream(device) if stream is None else stream
+    return ctypes.c_void_p(s.cuda_stream)
+
+
+def redlite_kv4_page_bytes(n_kv_heads: int, head_dim: int, page_size: int) -> int:
+    return int(lib().redlite_kv4_page_bytes(n_kv_heads, head_dim, page_size))
+
+
+def _kv4_pages(cache: torch.Tensor, n_kv_heads: int, head_dim: int, page_size: int) -> int:
+    """Pages a cache tensor holds, or -1 if it is not one of whole pages."""
+    b = redlite_kv4_page_bytes(n_kv_heads, head_dim, page_size)
+    n = cache.numel() * cache.element_size()
+    return n // b if b and n % b == 0 else -1
+
+
+def redlite_kv4_append(k: torch.Tensor, v: torch.Tensor, cu_tokens: torch.Tensor, start: torch.Tensor,
+                       block_table: torch.Tensor, cache: torch.Tensor, page_size: int,
+                       status: Optional[torch.Tensor] = None, stream=None) -> int:
+    """Store k, v [n_tokens, n_kv_heads, head_dim] as tokens start[s].. of each sequence in the 4-bit cache."""
+    n = start.numel()
+    if (not _mixer_ok((k, v), ((cu_tokens, torch.int32), (start, torch.int32), (block_table, torch.int32),
+                               (cache, torch.uint8), (status, torch.int32)))
+            or k.shape != v.shape or cu_tokens.numel() != n + 1 or block_table.dim() != 2 or block_table.shape[0] != n):
+        return REDLITE_EINVAL
+    T, H, D = k.shape
+    pages = _kv4_pages(cache, H, D, page_size)
+    if pages < 0:
+        return REDLITE_EUNSUPPORTED if redlite_kv4_page_bytes(H, D, page_size) == 0 else REDLITE_EINVAL
+    with torch.cuda.device(k.device):
+        return lib().redlite_kv4_append(_DTYPES[k.dtype], _ptr(k), _ptr(v), _row_stride(k), _row_stride(v),
+                                        _ptr(cu_tokens), _ptr(start), n, T, H, D, page_size, _ptr(block_table),
+                                        block_table.shape[1], pages, _ptr(cache), _ptr(status), _on(k.device, stream))
+
+
+def redlite_kv4_load(cache: torch.Tensor, page_size: int, block_table: torch.Tensor, cu_tokens: torch.Tensor,
+                     start: torch.Tensor, k: torch.Tensor, v: torch.Tensor, status: Optional[torch.Tensor] = None,
+                     stream=None) -> int:
+    """The values the cache stands for, into k and v [n_tokens, n_kv_heads, head_dim]."""
+    n = start.numel()
+    if (not _mixer_ok((k, v), ((cu_tokens, torch.int32), (start, torch.int32), (block_table, torch.int32),
+                               (cache, torch.uint8), (status, torch.int32)))
+            or k.shape != v.shape or cu_tokens.numel() != n + 1 or block_table.dim() != 2 or block_table.shape[0] != n):
+        return REDLITE_EINVAL
+    T, H, D = k.shape
+    pages = _kv4_pages(cache, H, D, page_size)
+    if pages < 0:
+        return REDLITE_EUNSUPPORTED if redlite_kv4_page_bytes(H, D, page_size) == 0 else REDLITE_EINVAL
+    with torch.cuda.device(k.device):
+        return lib().redlite_kv4_load(_DTYPES[k.dtype], _ptr(cache), H, D, page_size, _ptr(block_table),
+                                      block_table.shape[1], pages, _ptr(cu_tokens), _ptr(start), n, T, _ptr(k), _ptr(v),
+                                      _row_stride(k), _row_stride(v), _ptr(status), _on(k.device, stream))
+
+
+def redlite_kv4_decode_workspace_bytes(n_seqs: int, n_heads: int, n_kv_heads: int, head_dim: int) -> int:
+    return int(lib().redlite_kv4_decode_workspace_bytes(n_seqs, n_heads, n_kv_heads, head_dim))
+
+
+def redlite_kv4_decode(q: torch.Tensor, cache: torch.Tensor, page_size: int, block_table: torch.Tensor,
+                       lens: torch.Tensor, out: torch.Tensor, workspace: torch.Tensor, scale: float,
+                       status: Optional[torch.Tensor] = None, stream=None, n_kv_heads: Optional[int] = None) -> int:
+    """One query per sequence, q [n_seqs, n_heads, head_dim], over its first lens[s] cached tokens.
+    The cache is a [n_pages, n_kv_heads, ...] tensor, or flat with n_kv_heads given."""
+    if (not _mixer_ok((q, out), ((cache, torch.uint8), (block_table, torch.int32), (lens, torch.int32),
+                                 (status, torch.int32)))
+            or q.shape != out.shape or lens.numel() != q.shape[0] or block_table.dim() != 2
+            or block_table.shape[0] != q.shape[0] or not _dense(workspace, workspace.dtype, q.device)):
+        return REDLITE_EINVAL
+    B, Hq, D = q.shape
+    if n_kv_heads is None:
+        if cache.dim() < 2:
+            return REDLITE_EINVAL
+        n_kv_heads = cache.shape[1]
+    pages = _kv4_pages(cache, n_kv_heads, D, page_size)
+    if pages < 0:
+        return REDLITE_EUNSUPPORTED if redlite_kv4_page_bytes(n_kv_heads, D, page_size) == 0 else REDLITE_EINVAL
+    with torch.cuda.device(q.device):
+        return lib().redlite_kv4_decode(_DTYPES[q.dtype], _ptr(q), _row_stride(q), B, Hq, n_kv_heads, D, _ptr(cache),
+                                        page_size, _ptr(block_table), block_table.shape[1], pages, _ptr(lens),
+                                        float(scale), _ptr(out), _row_stride(out), _ptr(workspace),
+                                        workspace.numel() * workspace.element_size(), _ptr(status),
+                                        _on(q.device, stream))
 
 
 class SlotPool:

@@ -1,0 +1,623 @@
+// kv4_decode.cu -- attention of one query token per sequence over the paged
+// 4-bit key/value cache (redlite_kv4_decode).  ("Red Lite dev16 -- complete
+// full-attention parity", section "Pinned full-attention graph": grouped
+// heads over a K/V cache.)
+//
+//   s_t = scale * q . K_t,  p = softmax(s),  o = sum_t p_t V_t,
+//   K_t, V_t = m + d * code per group of 32 values.
+//
+// The floor is the cache's bytes (1.25 D per token and key/value head, both
+// sides), each read once; what stands beside it is the conversion of the
+// codes, so the kernel never forms the values.  Codes go to the tensor cores
+// as the exact bf16 numbers 1 + code / 16 (one shift and one and-or for two of
+// them), with
+//   q . K_t   = sum_g 16 d_tg (q_g . (1 + code / 16)) + (m_tg - 16 d_tg) sum(q_g)
+//   o of g    = sum_t (16 d_tg p_t) (code - 8) / 16 + sum_t p_t (m_tg + 8 d_tg):
+// steps and minima are applied in fp32 to the 16 x 8 products (keys) and to
+// the 16 probabilities (values), once per group of 32 values.  Queries are
+// split into bf16 parts that hold them exactly (1 part for bf16, 2 for fp16,
+// 3 for fp32); 16 d p and p are split into two parts (what is left out is at
+// most 2^-17 of each product).  Sums, maxima and the running softmax
+// statistics are fp32.
+//
+// Split: the units of all sequences (128 tokens of one key/value head and up
+// to 8 of its query heads) form one list, cut evenly over a fixed grid; a
+// block joins its eight warps (16 tokens each, tiles streamed into a
+// per-warp ring by bulk copies) at the end of each run of units and writes
+// either the output or one of its two partial results, which kv4_join_kernel
+// adds up in a fixed order: no atomics, nothing kept from call to call.
+#include "kv4.cuh"
+
+namespace redlite {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kUnit = 16 * kWarps;  // tokens of a unit
+constexpr float kLazy = 8.f;        // log2 by which scores may pass the reference before sums are rescaled
+
+struct DecArgs {
+  const void *q;
+  void *out;
+  int64_t q_stride, out_stride;
+  const uint8_t *cache;
+  const int32_t *table, *lens;
+  int n_seqs, n_heads, n_kv, ratio, hb_count;  // hb_count: blocks of 8 query heads per key/value head
+  int page_size, max_pages;
+  int64_t n_pages;
+  float scale_log2;
+  float *part;  // [2 grid][8 * D + 16]
+  int grid;
+  int32_t *status;
+};
+
+__device__ __forceinline__ int seq_units(const DecArgs &a, int s) {
+  const int n = __ldg(a.lens + s);
+  if (n <= 0 || (int64_t)n > (int64_t)a.max_pages * a.page_size) return 0;
+  return (n + kUnit - 1) / kUnit;
+}
+
+// Sum of the units of all sequences (of one head block), and where unit u of
+// the list over sequences falls: the sequence and the units in front of it.
+// Every thread of the block calls it; `sm` holds 4 + blockDim / 32 words.
+__device__ __forceinline__ int64_t scan_units(const DecArgs &a, int64_t *sm) {
+  // thread t counts sequences t * per .. ; their exclusive prefix in registers
+  const int per = (a.n_seqs + blockDim.x - 1) / blockDim.x;
+  const int s0 = min(a.n_seqs, (int)threadIdx.x * per), s1 = min(a.n_seqs, s0 + per);
+  int64_t mine = 0;
+  for (int s = s0; s < s1; ++s) mine += seq_units(a, s);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t inc = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += v;
+  }
+  if (lane == 31) sm[4 + warp] = inc;
+  __syncthreads();
+  int64_t base = 0, total = 0;
+  for (int w = 0; w < (int)(blockDim.x >> 5); ++w) {
+    if (w < warp) base += sm[4 + w];
+    total += sm[4 + w];
+  }
+  if (threadIdx.x == 0) sm[0] = total;
+  const int64_t first = base + inc - mine;  // units in front of sequence s0
+  // published for the caller: sm[1] target in, sm[2] sequence, sm[3] prefix
+  const int64_t target = sm[1];
+  if (mine && target >= first && target < first + mine) {
+    int64_t p = first;
+    for (int s = s0; s < s1; ++s) {
+      const int n = seq_units(a, s);
+      if (target < p + n) {
+        sm[2] = s, sm[3] = p;
+        break;
+      }
+      p += n;
+    }
+  }
+  __syncthreads();
+  return sm[0];
+}
+
+template <typename T>
+struct Splits {
+  static constexpr int n = 1;
+};
+template <>
+struct Splits<__half> {
+  static constexpr int n = 2;
+};
+template <>
+struct Splits<float> {
+  static constexpr int n = 3;
+};
+
+template <int D>
+struct DecSmem {
+  static constexpr int NG = D / 32;
+  static constexpr int kTile = 20 * D;
+  static constexpr int kStages = D == 256 ? 2 : 4;
+  static constexpr int kRing = kWarps * kStages * kTile;
+};
+
+template <typename T, int D>
+constexpr int dec_smem_bytes() {
+  return DecSmem<D>::kRing + Splits<T>::n * (D / 32) * 512 + (D / 32) * 32 + kWarps * 8 * 8 +
+         kWarps * DecSmem<D>::kStages * 8 + (4 + kWarps) * 8 + 32;
+}
+
+// (1 + code / 16) as bf16 pairs from nibble i of both halves of w.
+__device__ __forceinline__ uint32_t code_pair(uint32_t w, int i) {
+  const uint32_t x = i == 0 ? w << 3 : w >> (4 * i - 3);
+  return (x & 0x00780078u) | 0x3f803f80u;
+}
+// minus 1.5: (code - 8) / 16, exact
+__device__ __forceinline__ uint32_t centre(uint32_t v) {
+  uint32_t r;
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(0x3fc03fc0u));
+  return r;
+}
+__device__ __forceinline__ float h_lo(uint32_t v) { return __half2float(__ushort_as_half((uint16_t)v)); }
+__device__ __forceinline__ float h_hi(uint32_t v) { return __half2float(__ushort_as_half((uint16_t)(v >> 16))); }
+
+template <typename T, int D>
+__global__ void __launch_bounds__(32 * kWarps, 2) kv4_decode_kernel(const DecArgs a) {
+  using S = DecSmem<D>;
+  constexpr int NG = S::NG, NS = Splits<T>::n, kStages = S::kStages;
+  extern __shared__ __align__(128) uint8_t smem[];
+  uint8_t *ring_all = smem;
+  uint4 *qf = reinterpret_cast<uint4 *>(smem + S::kRing);             // [NS][NG][32]
+  float *qs = reinterpret_cast<float *>(qf + NS * NG * 32);          // [NG][8]
+  float2 *ml = reinterpret_cast<float2 *>(qs + NG * 8);              // [kWarps][8] {m, l}
+  uint64_t *bars = reinterpret_cast<uint64_t *>(ml + kWarps * 8);    // [kWarps][kStages]
+  int64_t *scan = reinterpret_cast<int64_t *>(bars + kWarps * kStages);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, c = lane & 3;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  uint64_t *bar = bars + warp * kStages;
+  uint8_t *ring = ring_all + warp * kStages * S::kTile;
+  if (lane == 0)
+    for (int i = 0; i < kStages; ++i) ptx::mbar_init(bar + i, 1);
+  ptx::mbar_fence_init();
+  // units of the whole call, then of this block
+  if (tid == 0) scan[1] = -1;
+  __syncthreads();
+  const int hh = a.n_kv * a.hb_count;
+  const int64_t total = scan_units(a, scan) * hh;
+  const int64_t parts = min((int64_t)a.grid, total);  // blocks that get units: at least one each
+  const bool idle = blockIdx.x >= parts;
+  const int64_t u_begin = idle ? 0 : total * blockIdx.x / parts, u_end = idle ? 0 : total * (blockIdx.x + 1) / parts;
+  if (blockIdx.x == 0)
+    for (int s = tid; s < a.n_seqs; s += blockDim.x) {
+      const int n = __ldg(a.lens + s);
+      if (n < 0 || (int64_t)n > (int64_t)a.max_pages * a.page_size) set_status(a.status, REDLITE_STATUS_BAD_LENGTH);
+    }
+  if (u_begin >= u_end) return;
+  if (tid == 0) scan[1] = u_begin / hh;
+  __syncthreads();
+  scan_units(a, scan);
+  int seq = (int)scan[2];
+  int64_t seq_base = scan[3];  // units (of one head block) in front of it
+  __syncthreads();
+
+  uint32_t phase = 0;  // bit i: parity of stage i's next completion
+  int64_t u = u_begin;
+  while (u < u_end) {
+    int n_units = seq_units(a, seq);
+    while ((seq_base + n_units) * hh <= u) {
+      seq_base += n_units;
+      n_units = seq_units(a, ++seq);
+    }
+    const int64_t in_seq = u - seq_base * hh;
+    const int block_of = (int)(in_seq / n_units), j0 = (int)(in_seq % n_units);
+    const int j1 = (int)min((int64_t)n_units, j0 + (u_end - u));
+    const int kvh = block_of / a.hb_count, hb = block_of % a.hb_count;
+    const int len = __ldg(a.lens + seq);
+    const int head0 = kvh * a.ratio + hb * 8, n_h = min(8, a.ratio - hb * 8);
+
+    // ---- the tiles of this warp: tile0 + kWarps * i, i < n_it
+    const int tile0 = j0 * kWarps + warp, n_tiles = (len + 15) >> 4;
+    const int tile_end = min(n_tiles, j1 * kWarps);
+    const int n_it = tile0 < tile_end ? (tile_end - tile0 + kWarps - 1) / kWarps : 0;
+    const int tiles_per_page = a.page_size >> 4;
+    const int32_t *table = a.table + (int64_t)seq * a.max_pages;
+    // lane i holds the page of tile number `batch + i`
+    int batch = -32;
+    int64_t my_page = -1;
+    auto issue = [&](int it) {
+      if (it - batch >= 32) {
+        batch = it;
+        const int t = tile0 + kWarps * (it + lane);
+        my_page = it + lane < n_it ? (int64_t)__ldg(table + t / tiles_per_page) : -1;
+        if (it + lane < n_it && (my_page < 0 || my_page >= a.n_pages)) {
+          set_status(a.status, REDLITE_STATUS_BAD_PAGE);
+          my_page = -1;
+        }
+      }
+      const int64_t page = __shfl_sync(0xffffffffu, my_page, it - batch);
+      if (lane == 0) {
+        const int st = it % kStages, t = tile0 + kWarps * it;
+        if (page >= 0) {
+          ptx::mbar_expect_tx(bar + st, S::kTile);
+          ptx::bulk_g2s(ring + st * S::kTile,
+                        a.cache + kv4_tile_offset<D>(page, a.n_kv, kvh, a.page_size, t % tiles_per_page), S::kTile,
+                        bar + st);
+        } else {
+          ptx::mbar_arrive(bar + st);  // nothing is read: the tile is masked below
+        }
+      }
+      return page >= 0;
+    };
+    uint32_t good = 0;  // bit i: the tile in stage i is real
+#pragma unroll
+    for (int i = 0; i < kStages; ++i)
+      if (i < n_it) good |= (uint32_t)issue(i) << i;
+
+    // ---- queries of the block's heads as bf16 parts, and their sums per group
+    for (int i = tid; i < NG * 32; i += 32 * kWarps) {
+      const int g = i >> 5, rr = (i >> 2) & 7, cc = i & 3;
+      float x[8];
+      if (rr < n_h) {
+        load8<T>((const T *)a.q + (int64_t)seq * a.q_stride + (int64_t)(head0 + rr) * D + 32 * g + 8 * cc, x);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = 0.f;
+      }
+      float sum = ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      if (cc == 0) qs[g * 8 + rr] = sum;
+#pragma unroll
+      for (int p = 0; p < NS; ++p) {
+        uint4 w;  // pairs (0,4) (1,5) (2,6) (3,7): nibble i of both halves of a code word
+        w.x = pack_bf16(x[0], x[4]), w.y = pack_bf16(x[1], x[5]);
+        w.z = pack_bf16(x[2], x[6]), w.w = pack_bf16(x[3], x[7]);
+        qf[(p * NG + g) * 32 + (i & 31)] = w;
+        x[0] -= bf16_lo(w.x), x[4] -= bf16_hi(w.x), x[1] -= bf16_lo(w.y), x[5] -= bf16_hi(w.y);
+        x[2] -= bf16_lo(w.z), x[6] -= bf16_hi(w.z), x[3] -= bf16_lo(w.w), x[7] -= bf16_hi(w.w);
+      }
+    }
+    __syncthreads();
+
+    float acc[NG][2][4], accm[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int g = 0; g < NG; ++g)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[g][e][i] = 0.f;
+    float m_run = -INFINITY, l_run = 0.f;  // of query head r; l over this thread's tokens
+
+    for (int it = 0; it < n_it; ++it) {
+      const int st = it % kStages;
+      const uint32_t tile = ptx::smem_u32(ring + st * S::kTile);
+      const bool came = ptx::mbar_wait_suspend(bar + st, (phase >> st) & 1u);
+      if (!__all_sync(0xffffffffu, came)) set_status(a.status, REDLITE_STATUS_TIMEOUT);
+      phase ^= 1u << st;
+      const int tok0 = 16 * (tile0 + kWarps * it);
+      const int live = ((good >> st) & 1u) ? len - tok0 : 0;  // tokens of this tile that count
+      // ---- scores: C[token][head] over the groups
+      float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int gq = 0; gq < NG / 4; ++gq) {
+        const uint4 w0 = ptx::lds128(tile + gq * 512 + lane * 16);               // token r
+        const uint4 w1 = ptx::lds128(tile + (NG / 4 + gq) * 512 + lane * 16);    // token r + 8
+        const uint4 k0 = ptx::lds128(tile + 8 * D + r * (NG * 4) + gq * 16);      // {d, m} of four groups
+        const uint4 k1 = ptx::lds128(tile + 8 * D + (r + 8) * (NG * 4) + gq * 16);
+        const uint32_t wa[4] = {w0.x, w0.y, w0.z, w0.w}, wb[4] = {w1.x, w1.y, w1.z, w1.w};
+        const uint32_t ka[4] = {k0.x, k0.y, k0.z, k0.w}, kb[4] = {k1.x, k1.y, k1.z, k1.w};
+#pragma unroll
+        for (int gg = 0; gg < 4; ++gg) {
+          const int g = gq * 4 + gg;
+          uint32_t A0[4], A1[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) A0[i] = code_pair(wa[gg], i), A1[i] = code_pair(wb[gg], i);
+          float x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int p = 0; p < NS; ++p) {
+            const uint4 b = qf[(p * NG + g) * 32 + lane];
+            mma_bf16(x, A0[0], A1[0], A0[1], A1[1], b.x, b.y);
+            mma_bf16(x, A0[2], A1[2], A0[3], A1[3], b.z, b.w);
+          }
+          const float2 sum = *reinterpret_cast<const float2 *>(qs + g * 8 + 2 * c);
+          const float da = 16.f * h_lo(ka[gg]), db = 16.f * h_lo(kb[gg]);
+          const float ma = h_hi(ka[gg]) - da, mb = h_hi(kb[gg]) - db;
+          s[0] = fmaf(da, x[0], fmaf(ma, sum.x, s[0]));
+          s[1] = fmaf(da, x[1], fmaf(ma, sum.y, s[1]));
+          s[2] = fmaf(db, x[2], fmaf(mb, sum.x, s[2]));
+          s[3] = fmaf(db, x[3], fmaf(mb, sum.y, s[3]));
+        }
+      }
+      // ---- to the layout of the second product: head r, tokens 2c, 2c+1, 2c+8, 2c+9
+      float p[4];
+      {
+        const int src = 8 * c + (r >> 1);
+        const float a0 = __shfl_sync(0xffffffffu, s[0], src), a1 = __shfl_sync(0xffffffffu, s[1], src);
+        const float b0 = __shfl_sync(0xffffffffu, s[0], src + 4), b1 = __shfl_sync(0xffffffffu, s[1], src + 4);
+        const float c0 = __shfl_sync(0xffffffffu, s[2], src), c1 = __shfl_sync(0xffffffffu, s[3], src);
+        const float d0 = __shfl_sync(0xffffffffu, s[2], src + 4), d1 = __shfl_sync(0xffffffffu, s[3], src + 4);
+        p[0] = (r & 1) ? a1 : a0, p[1] = (r & 1) ? b1 : b0;
+        p[2] = (r & 1) ? c1 : c0, p[3] = (r & 1) ? d1 : d0;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) p[i] = 2 * c + (i & 1) + 8 * (i >> 1) < live ? p[i] * a.scale_log2 : -INFINITY;
+      float mx = fmaxf(fmaxf(p[0], p[1]), fmaxf(p[2], p[3]));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      // rescale only when a score passes the reference by 2^8 (or the first
+      // one comes): the sums stay far inside fp32 either way
+      if (__any_sync(0xffffffffu, mx > m_run + kLazy || (m_run == -INFINITY && mx > -INFINITY))) {
+        const float m_new = fmaxf(m_run, mx);
+        const float f = m_run == -INFINITY ? 0.f : ex2(m_run - m_new);
+        l_run *= f;
+        m_run = m_new;
+        const float f0 = __shfl_sync(0xffffffffu, f, 8 * c), f1 = __shfl_sync(0xffffffffu, f, 8 * c + 4);
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            acc[g][e][0] *= f0, acc[g][e][1] *= f1, acc[g][e][2] *= f0, acc[g][e][3] *= f1;
+        accm[0] *= f0, accm[1] *= f1, accm[2] *= f0, accm[3] *= f1;
+      }
+      const float ref = m_run == -INFINITY ? 0.f : m_run;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) p[i] = ex2(p[i] - ref), l_run += p[i];
+      // ---- values
+      const uint32_t vs = tile + 18 * D, vm = tile + 19 * D;
+      int tk[4];
+      bool on[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) tk[i] = 2 * c + (i & 1) + 8 * (i >> 1), on[i] = tk[i] < live;
+      uint32_t ph[2], pl[2];
+      split_bf16(p[0], p[1], ph[0], pl[0]);
+      split_bf16(p[2], p[3], ph[1], pl[1]);
+      {
+        // group r's m + 8 d of the four tokens (rows r: high part, rows r + 8: low part)
+        float mid[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int g = r & (NG - 1);
+          const float d = h_lo(ptx::lds16(vs + (tk[i] * NG + g) * 2)), m = h_lo(ptx::lds16(vm + (tk[i] * NG + g) * 2));
+          mid[i] = on[i] && r < NG ? fmaf(8.f, d, m) : 0.f;
+        }
+        uint32_t h0, l0, h1, l1;
+        split_bf16(mid[0], mid[1], h0, l0);
+        split_bf16(mid[2], mid[3], h1, l1);
+        mma_bf16(accm, h0, l0, h1, l1, ph[0], ph[1]);
+        mma_bf16(accm, h0, l0, h1, l1, pl[0], pl[1]);
+      }
+      uint32_t vw[4][NG / 2], dw[4][NG / 2];  // codes and steps of the four tokens
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        // the code unit of slot i = 2 h + b is token 2 c + b + 8 h, as tk[i]
+        if (NG == 8) {
+          const uint4 v = ptx::lds128(tile + 10 * D + i * 512 + lane * 16), d = ptx::lds128(vs + tk[i] * 16);
+          vw[i][0] = v.x, vw[i][1] = v.y, vw[i][NG / 2 - 2] = v.z, vw[i][NG / 2 - 1] = v.w;
+          dw[i][0] = d.x, dw[i][1] = d.y, dw[i][NG / 2 - 2] = d.z, dw[i][NG / 2 - 1] = d.w;
+        } else {
+          const uint2 v = ptx::lds64(tile + 10 * D + (i >> 1) * 512 + lane * 16 + (i & 1) * 8);
+          const uint2 d = ptx::lds64(vs + tk[i] * 8);
+          vw[i][0] = v.x, vw[i][1] = v.y, dw[i][0] = d.x, dw[i][1] = d.y;
+        }
+        p[i] *= 16.f;
+      }
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        float pd[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float d = (g & 1) ? h_hi(dw[i][g >> 1]) : h_lo(dw[i][g >> 1]);
+          pd[i] = on[i] ? p[i] * d : 0.f;
+        }
+        uint32_t bh0, bl0, bh1, bl1;
+        split_bf16(pd[0], pd[1], bh0, bl0);
+        split_bf16(pd[2], pd[3], bh1, bl1);
+        const uint32_t sel = (g & 1) ? 0x7632u : 0x5410u;
+        const uint32_t X = __byte_perm(vw[0][g >> 1], vw[1][g >> 1], sel);
+        const uint32_t Y = __byte_perm(vw[2][g >> 1], vw[3][g >> 1], sel);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t a0 = centre(code_pair(X, 2 * e)), a1 = centre(code_pair(X, 2 * e + 1));
+          const uint32_t a2 = centre(code_pair(Y, 2 * e)), a3 = centre(code_pair(Y, 2 * e + 1));
+          mma_bf16(acc[g][e], a0, a1, a2, a3, bh0, bh1);
+          mma_bf16(acc[g][e], a0, a1, a2, a3, bl0, bl1);
+        }
+      }
+      // ---- the stage is free again
+      if (it + kStages < n_it) {
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        const uint32_t ok = issue(it + kStages);
+        good = (good & ~(1u << st)) | (ok << st);
+      }
+    }
+
+    // ---- join the warps (the rings are drained: they hold the results now)
+    l_run += __shfl_xor_sync(0xffffffffu, l_run, 1);
+    l_run += __shfl_xor_sync(0xffffffffu, l_run, 2);
+    if (c == 0) ml[warp * 8 + r] = make_float2(m_run, l_run);
+    __syncwarp();
+    float *mine = reinterpret_cast<float *>(ring);  // [8 heads][D]
+    accm[0] += accm[2], accm[1] += accm[3];  // high and low parts
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      // group g's sum over m + 8 d sits in the lanes of row g
+      const float g0 = __shfl_sync(0xffffffffu, accm[0], g * 4 + c), g1 = __shfl_sync(0xffffffffu, accm[1], g * 4 + c);
+      float *h0 = mine + (2 * c) * D + 32 * g + 4 * r, *h1 = h0 + D;
+      *reinterpret_cast<float4 *>(h0) =
+          make_float4(acc[g][0][0] + g0, acc[g][0][2] + g0, acc[g][1][0] + g0, acc[g][1][2] + g0);
+      *reinterpret_cast<float4 *>(h1) =
+          make_float4(acc[g][0][1] + g1, acc[g][0][3] + g1, acc[g][1][1] + g1, acc[g][1][3] + g1);
+    }
+    __syncthreads();
+    const bool whole = j0 == 0 && j1 == n_units;
+    float *part = a.part + (int64_t)(2 * blockIdx.x + (j0 > 0 ? 0 : 1)) * (8 * D + 16);
+    for (int i = tid; i < 8 * D / 4; i += 32 * kWarps) {
+      const int h = i / (D / 4), d4 = i % (D / 4);
+      if (h >= n_h) continue;
+      float m = -INFINITY, l = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) m = fmaxf(m, ml[w * 8 + h].x);
+      const float base = m == -INFINITY ? 0.f : m;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float2 v = ml[w * 8 + h];
+        const float f = ex2(v.x - base);
+        const float4 x =
+            *reinterpret_cast<const float4 *>(ring_all + w * kStages * S::kTile + (size_t)(h * D + 4 * d4) * 4);
+        if (v.x > -INFINITY) {
+          l = fmaf(f, v.y, l);
+          o.x = fmaf(f, x.x, o.x), o.y = fmaf(f, x.y, o.y), o.z = fmaf(f, x.z, o.z), o.w = fmaf(f, x.w, o.w);
+        }
+      }
+      if (whole) {
+        const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+        T *dst = (T *)a.out + (int64_t)seq * a.out_stride + (int64_t)(head0 + h) * D + 4 * d4;
+        dst[0] = from_f32<T>(o.x * inv), dst[1] = from_f32<T>(o.y * inv);
+        dst[2] = from_f32<T>(o.z * inv), dst[3] = from_f32<T>(o.w * inv);
+      } else {
+        reinterpret_cast<float4 *>(part)[i] = o;
+        if (d4 == 0) *reinterpret_cast<float2 *>(part + 8 * D + 2 * h) = make_float2(m, l);
+      }
+    }
+    ptx::fence_proxy_async_smem();
+    __syncthreads();
+    u += j1 - j0;
+  }
+}
+
+// One block per sequence and query head: adds the partial results of a head
+// block's units in the order of the blocks that made them (four runs of
+// blocks, then the runs), and writes zeros for a sequence without tokens.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) kv4_join_kernel(const DecArgs a) {
+  constexpr int kRuns = 1024 / D, kPart = 8 * D + 16;
+  __shared__ int64_t scan[4 + 8];
+  __shared__ float red[8];
+  __shared__ float4 sum[kRuns][D / 4];
+  __shared__ float run_l[kRuns];
+  const int tid = threadIdx.x;
+  const int seq = blockIdx.x / a.n_heads, head = blockIdx.x % a.n_heads;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int n_units = seq_units(a, seq);
+  T *dst = (T *)a.out + (int64_t)seq * a.out_stride + (int64_t)head * D;
+  if (n_units == 0) {
+    if (tid < D) dst[tid] = from_f32<T>(0.f);
+    return;
+  }
+  if (tid == 0) scan[1] = -1;
+  __syncthreads();
+  // units in front of this sequence
+  int64_t before = 0;
+  for (int s = tid; s < seq; s += blockDim.x) before += seq_units(a, s);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+  __shared__ int64_t front[8];
+  if ((tid & 31) == 0) front[tid >> 5] = before;
+  const int hh = a.n_kv * a.hb_count;
+  const int64_t total = scan_units(a, scan) * hh;
+  before = 0;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) before += front[w];
+  const int kvh = head / a.ratio, in_kv = head % a.ratio, hb = in_kv >> 3, h = in_kv & 7;
+  const int64_t u0 = before * hh + (int64_t)(kvh * a.hb_count + hb) * n_units, u1 = u0 + n_units - 1;
+  // block of unit u: the i with total * i / parts <= u < total * (i + 1) / parts
+  const int64_t parts = min((int64_t)a.grid, total);
+  const int i0 = (int)(((u0 + 1) * parts - 1) / total), i1 = (int)(((u1 + 1) * parts - 1) / total);
+  if (i0 == i1) return;  // one block saw all of it and wrote the output
+  auto part = [&](int i) { return a.part + (int64_t)(2 * i + (i == i0 ? 1 : 0)) * kPart; };
+  float m = -INFINITY;
+  for (int i = i0 + tid; i <= i1; i += blockDim.x) m = fmaxf(m, __ldg(part(i) + 8 * D + 2 * h));
+#pragma unroll
+  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if ((tid & 31) == 0) red[tid >> 5] = m;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 8; ++w) m = fmaxf(m, red[w]);
+  const float base = m == -INFINITY ? 0.f : m;
+  const int run = tid / (D / 4), d4 = tid % (D / 4);
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  float l = 0.f;
+#pragma unroll 4
+  for (int i = i0 + run; i <= i1; i += kRuns) {
+    const float *p = part(i);
+    const float2 v = __ldg(reinterpret_cast<const float2 *>(p + 8 * D + 2 * h));
+    const float4 x = __ldg(reinterpret_cast<const float4 *>(p + h * D) + d4);
+    if (v.x > -INFINITY) {
+      const float f = ex2(v.x - base);
+      l = fmaf(f, v.y, l);
+      o.x = fmaf(f, x.x, o.x), o.y = fmaf(f, x.y, o.y), o.z = fmaf(f, x.z, o.z), o.w = fmaf(f, x.w, o.w);
+    }
+  }
+  sum[run][d4] = o;
+  if (d4 == 0) run_l[run] = l;
+  __syncthreads();
+  if (run == 0) {
+    for (int k = 1; k < kRuns; ++k) {
+      const float4 x = sum[k][d4];
+      o.x += x.x, o.y += x.y, o.z += x.z, o.w += x.w;
+      l += run_l[k];
+    }
+    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+    dst[4 * d4] = from_f32<T>(o.x * inv), dst[4 * d4 + 1] = from_f32<T>(o.y * inv);
+    dst[4 * d4 + 2] = from_f32<T>(o.z * inv), dst[4 * d4 + 3] = from_f32<T>(o.w * inv);
+  }
+}
+
+template <typename T, int D>
+cudaError_t launch_decode(const DecArgs &a, cudaStream_t s) {
+  constexpr int smem = dec_smem_bytes<T, D>();
+  cudaError_t e =
+      cudaFuncSetAttribute(kv4_decode_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kv4_decode_kernel<T, D><<<a.grid, 32 * kWarps, smem, s>>>(a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(a.n_seqs * a.n_heads));
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at, cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv4_join_kernel<T, D>, a);
+}
+template <typename T>
+cudaError_t launch_decode_t(const DecArgs &a, int D, cudaStream_t s) {
+  return D == 256 ? launch_decode<T, 256>(a, s) : launch_decode<T, 128>(a, s);
+}
+
+// Blocks of a call: two per multiprocessor (what the kernel's shared memory
+// and registers allow), for any sizes.
+constexpr int kMaxGrid = 2 * 256;
+
+}  // namespace
+}  // namespace redlite
+
+using namespace redlite;
+
+extern "C" size_t redlite_kv4_decode_workspace_bytes(int32_t n_seqs, int32_t n_heads, int32_t n_kv_heads,
+                                                     int32_t head_dim) {
+  if (n_seqs < 0 || n_kv_heads < 1 || n_heads < 1 || n_heads > 4096 || n_heads % n_kv_heads || !kv4_shape_ok(head_dim, 16))
+    return 0;
+  return (size_t)2 * kMaxGrid * (8 * head_dim + 16) * sizeof(float);
+}
+
+extern "C" int redlite_kv4_decode(int32_t dtype, const void *q, int64_t q_stride, int32_t n_seqs, int32_t n_heads,
+                                  int32_t n_kv_heads, int32_t head_dim, const void *cache, int32_t page_size,
+                                  const int32_t *block_table, int32_t max_pages, int64_t n_pages,
+                                  const int32_t *lens, float scale, void *out, int64_t out_stride, void *workspace,
+                                  size_t workspace_bytes, int32_t *status, void *stream) {
+  if (!dtype_ok(dtype) || n_seqs < 0 || n_heads < 1 || n_heads > 4096 || n_kv_heads < 1 || n_kv_heads > 1024 ||
+      n_heads % n_kv_heads)
+    return REDLITE_EINVAL;
+  if (!kv4_shape_ok(head_dim, page_size)) return REDLITE_EUNSUPPORTED;
+  if (!(scale > 0.f) || !(scale < INFINITY)) return REDLITE_EINVAL;
+  if (n_seqs == 0) return REDLITE_OK;
+  if (max_pages < 1 || n_pages < 1 || !q || !cache || !block_table || !lens || !out || !workspace) return REDLITE_EINVAL;
+  if (!aligned16(q) || !aligned16(cache) || !aligned16(out) || !aligned16(workspace)) return REDLITE_EINVAL;
+  const int64_t row = (int64_t)n_heads * head_dim;
+  if (!stride_ok(q_stride, row, dtype) || !stride_ok(out_stride, row, dtype)) return REDLITE_EINVAL;
+  if ((int64_t)n_seqs * n_heads >= ((int64_t)1 << 31) - 1) return REDLITE_EUNSUPPORTED;
+  if (workspace_bytes < redlite_kv4_decode_workspace_bytes(n_seqs, n_heads, n_kv_heads, head_dim)) return REDLITE_ENOMEM;
+  const int sms = sm_count();
+  if (sms <= 0) return REDLITE_ECUDA;
+  DecArgs a;
+  a.q = q, a.out = out, a.q_stride = q_stride, a.out_stride = out_stride;
+  a.cache = (const uint8_t *)cache, a.table = block_table, a.lens = lens;
+  a.n_seqs = n_seqs, a.n_heads = n_heads, a.n_kv = n_kv_heads, a.ratio = n_heads / n_kv_heads;
+  a.hb_count = (a.ratio + 7) / 8;
+  a.page_size = page_size, a.max_pages = max_pages, a.n_pages = n_pages;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.part = (float *)workspace;
+  a.status = status;
+  // no more blocks than units the longest lengths could give
+  const int64_t cap = (int64_t)n_seqs * n_kv_heads * a.hb_count * (((int64_t)max_pages * page_size + kUnit - 1) / kUnit);
+  a.grid = (int)std::min<int64_t>(std::min(2 * sms, kMaxGrid), cap);
+  cudaStream_t s = (cudaStream_t)stream;
+  cudaError_t e;
+  if (dtype == REDLITE_T_F32) e = launch_decode_t<float>(a, head_dim, s);
+  else if (dtype == REDLITE_T_BF16) e = launch_decode_t<__nv_bfloat16>(a, head_dim, s);
+  else e = launch_decode_t<__half>(a, head_dim, s);
+  return e == cudaSuccess ? REDLITE_OK : REDLITE_ECUDA;
+}
