@@ -414,6 +414,44 @@ int redlite_kv4_decode(int32_t dtype, const void *q, int64_t q_stride, int32_t n
                        void *out, int64_t out_stride, void *workspace, size_t workspace_bytes, int32_t *status,
                        void *stream);
 
+/* The gated delta rule.  Per value head h (key head h / (n_v_heads /
+ * n_k_heads)) and token, with the state S [dk, dv]:
+ *   S <- exp(g) S;  S <- S + k (beta (v - S^T k))^T;  out = scale * S^T q
+ *   q, k      device [rows, n_k_heads * dk]; v, out [rows, n_v_heads * dv]
+ *   g, beta   device fp32 [rows, n_v_heads], contiguous; g is the log of the
+ *             decay (at most 0 in use; -infinity clears the state)
+ *   qk_eps    >= 0: q and k are divided by sqrt(sum of squares + qk_eps)
+ *             per head first; negative: used as given
+ *   dk, dv    64 or 128 each
+ *   state_in  device fp32 [n_slots, n_v_heads, dk, dv], 16-byte aligned, or
+ *             NULL for zeros; state_out the same shape, written; they may be
+ *             one buffer (each slot is read before it is written)
+ *   slots     device int32 [n_seqs], the slot of each sequence, or NULL for
+ *             slot s = sequence s.  A slot outside [0, n_slots), or one that
+ *             an earlier sequence of the call names too, is reported: the
+ *             sequence's outputs become zeros and no state is written for it.
+ * Slots that no sequence names are left as they are; a sequence without
+ * tokens copies its state.
+ *
+ * redlite_delta_prefill runs packed sequences of any lengths in chunks of 64
+ * tokens (with n_tokens = 0 it copies the states); workspace 256-byte
+ * aligned.  A cu that does not ascend within 0 .. n_tokens is reported; the
+ * sequences it breaks are skipped, their states not written.  redlite_delta_step runs one token per
+ * sequence: row s is sequence s. */
+size_t redlite_delta_workspace_bytes(int32_t n_tokens, int32_t n_seqs, int32_t n_k_heads, int32_t n_v_heads, int32_t dk,
+                                     int32_t dv);
+int redlite_delta_prefill(int32_t dtype, const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                          const void *v, int64_t v_stride, const float *g, const float *beta, const int32_t *cu,
+                          int32_t n_seqs, int32_t n_tokens, int32_t n_k_heads, int32_t n_v_heads, int32_t dk,
+                          int32_t dv, float scale, float qk_eps, const float *state_in, float *state_out,
+                          const int32_t *slots, int64_t n_slots, void *out, int64_t out_stride, void *workspace,
+                          size_t workspace_bytes, int32_t *status, void *stream);
+int redlite_delta_step(int32_t dtype, const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                       int64_t v_stride, const float *g, const float *beta, int32_t n_seqs, int32_t n_k_heads,
+                       int32_t n_v_heads, int32_t dk, int32_t dv, float scale, float qk_eps, const float *state_in,
+                       float *state_out, const int32_t *slots, int64_t n_slots, void *out, int64_t out_stride,
+                       int32_t *status, void *stream);
+
 /* ---------------------------------------------------------------- slot pool
  * The bounded, top-k-aware LRU pool of expert slots ("Red Metal dev8",
  * steps 1-3: the hard-bounded LRU makes every selected expert resident,

@@ -109,6 +109,14 @@ EXPORTS = {
     "redlite_kv4_decode": (ctypes.c_int, [_i32, _c_void_p, _i64, _i32, _i32, _i32, _i32, _c_void_p, _i32, _c_void_p,
                                           _i32, _i64, _c_void_p, ctypes.c_float, _c_void_p, _i64, _c_void_p,
                                           ctypes.c_size_t, _c_void_p, _c_void_p]),
+    "redlite_delta_workspace_bytes": (ctypes.c_size_t, [_i32] * 6),
+    "redlite_delta_prefill": (ctypes.c_int, [_i32, _c_void_p, _i64, _c_void_p, _i64, _c_void_p, _i64, _c_void_p,
+                                             _c_void_p, _c_void_p, _i32, _i32, _i32, _i32, _i32, _i32, ctypes.c_float,
+                                             ctypes.c_float, _c_void_p, _c_void_p, _c_void_p, _i64, _c_void_p, _i64,
+                                             _c_void_p, ctypes.c_size_t, _c_void_p, _c_void_p]),
+    "redlite_delta_step": (ctypes.c_int, [_i32, _c_void_p, _i64, _c_void_p, _i64, _c_void_p, _i64, _c_void_p, _c_void_p,
+                                          _i32, _i32, _i32, _i32, _i32, ctypes.c_float, ctypes.c_float, _c_void_p,
+                                          _c_void_p, _c_void_p, _i64, _c_void_p, _i64, _c_void_p, _c_void_p]),
     "redlite_moe_pack_matrix": (ctypes.c_int, [ctypes.c_int32, ctypes.c_int64, ctypes.c_int64, _c_void_p,
                                                _c_void_p]),
     "redlite_moe_dequant": (ctypes.c_int, [ctypes.c_int32, _c_void_p, ctypes.c_int64, ctypes.c_int64, _c_void_p,
@@ -399,6 +407,57 @@ def redlite_kv4_decode(q: torch.Tensor, cache: torch.Tensor, page_size: int, blo
                                         float(scale), _ptr(out), _row_stride(out), _ptr(workspace),
                                         workspace.numel() * workspace.element_size(), _ptr(status),
                                         _on(q.device, stream))
+
+
+def redlite_delta_workspace_bytes(n_tokens: int, n_seqs: int, n_k_heads: int, n_v_heads: int, dk: int,
+                                  dv: int) -> int:
+    return int(lib().redlite_delta_workspace_bytes(n_tokens, n_seqs, n_k_heads, n_v_heads, dk, dv))
+
+
+def _delta_ok(q, k, v, g, beta, state_in, state_out, slots, out, status, n_seqs) -> bool:
+    f = torch.float32
+    if not _mixer_ok((q, k, v, out), ((g, f), (beta, f), (state_in, f), (state_out, f), (slots, torch.int32),
+                                      (status, torch.int32))):
+        return False
+    rows, hv, dv = v.shape
+    return (q.shape == k.shape and q.shape[0] == rows and out.shape == v.shape and g.shape == (rows, hv)
+            and beta.shape == (rows, hv) and state_out.dim() == 4 and state_out.shape[1:] == (hv, q.shape[2], dv)
+            and (state_in is None or state_in.shape == state_out.shape) and (slots is None or slots.numel() == n_seqs))
+
+
+def redlite_delta_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor,
+                          cu: torch.Tensor, state_in: Optional[torch.Tensor], state_out: torch.Tensor,
+                          slots: Optional[torch.Tensor], out: torch.Tensor, workspace: torch.Tensor, scale: float,
+                          qk_eps: float = -1.0, status: Optional[torch.Tensor] = None, stream=None) -> int:
+    """The gated delta rule over packed sequences: q, k [rows, n_k_heads, dk]; v, out [rows, n_v_heads, dv];
+    g, beta [rows, n_v_heads]; states [n_slots, n_v_heads, dk, dv]."""
+    n = cu.numel() - 1
+    if (n < 0 or not _delta_ok(q, k, v, g, beta, state_in, state_out, slots, out, status, n)
+            or not _dense(cu, torch.int32, q.device) or not _dense(workspace, workspace.dtype, q.device)):
+        return REDLITE_EINVAL
+    with torch.cuda.device(q.device):
+        return lib().redlite_delta_prefill(
+            _DTYPES[q.dtype], _ptr(q), _row_stride(q), _ptr(k), _row_stride(k), _ptr(v), _row_stride(v), _ptr(g),
+            _ptr(beta), _ptr(cu), n, q.shape[0], q.shape[1], v.shape[1], q.shape[2], v.shape[2], float(scale),
+            float(qk_eps), _ptr(state_in), _ptr(state_out), _ptr(slots), state_out.shape[0], _ptr(out),
+            _row_stride(out), _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(status),
+            _on(q.device, stream))
+
+
+def redlite_delta_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor,
+                       state_in: Optional[torch.Tensor], state_out: torch.Tensor, slots: Optional[torch.Tensor],
+                       out: torch.Tensor, scale: float, qk_eps: float = -1.0, status: Optional[torch.Tensor] = None,
+                       stream=None) -> int:
+    """One token per sequence (row s is sequence s); arguments as redlite_delta_prefill."""
+    n = q.shape[0]
+    if not _delta_ok(q, k, v, g, beta, state_in, state_out, slots, out, status, n):
+        return REDLITE_EINVAL
+    with torch.cuda.device(q.device):
+        return lib().redlite_delta_step(
+            _DTYPES[q.dtype], _ptr(q), _row_stride(q), _ptr(k), _row_stride(k), _ptr(v), _row_stride(v), _ptr(g),
+            _ptr(beta), n, q.shape[1], v.shape[1], q.shape[2], v.shape[2], float(scale), float(qk_eps), _ptr(state_in),
+            _ptr(state_out), _ptr(slots), state_out.shape[0], _ptr(out), _row_stride(out), _ptr(status),
+            _on(q.device, stream))
 
 
 class SlotPool:

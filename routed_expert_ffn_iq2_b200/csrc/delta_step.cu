@@ -1,0 +1,171 @@
+// delta_step.cu -- one token of the gated delta rule per sequence
+// (redlite_delta_step).  ("Red Lite dev15 -- DeltaNet projection bring-up",
+// section "Field-derived recurrent dimensions": Q/K norm, the delta update
+// on the recurrent state.)
+//
+//   S <- a S,  d = beta (v - S^T k),  S <- S + k d^T,  o = scale S^T q
+// with a = exp(g).  The floor is the state, read once and written once
+// (2 x 64 KB per head at 128 x 128), so it is held in registers between: one
+// pass forms S^T k and S^T q together, and
+//   d = beta (v - a S^T k),  o = scale (a S^T q + (q . k) d)
+// needs no second one.  A block owns 32 columns of one head's state (rows of
+// 128 bytes, 16 KB): a single sequence of 32 heads spreads over 128 blocks,
+// and in large batches some ten blocks per multiprocessor keep 16 KB each in
+// flight.  All sums are fp32.
+#include "delta.cuh"
+
+namespace redlite {
+
+int delta_check(int32_t dtype, const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                int64_t v_stride, const float *g, const float *beta, int32_t n_seqs, int64_t rows, int32_t n_k,
+                int32_t n_v, int32_t dk, int32_t dv, float scale, const float *state_in, const float *state_out,
+                const int32_t *slots, int64_t n_slots, const void *out, int64_t out_stride) {
+  if (!dtype_ok(dtype) || n_seqs < 0 || rows < 0) return REDLITE_EINVAL;
+  if (n_k < 1 || n_v < 1 || n_v > 1024 || n_v % n_k || dk < 1 || dv < 1) return REDLITE_EINVAL;
+  if ((dk != 64 && dk != 128) || (dv != 64 && dv != 128)) return REDLITE_EUNSUPPORTED;
+  if (!(scale > -INFINITY && scale < INFINITY)) return REDLITE_EINVAL;
+  if (n_seqs == 0) return REDLITE_OK;
+  if (!state_out || !aligned16(state_in) || !aligned16(state_out) || n_slots < 1) return REDLITE_EINVAL;
+  if (!slots && n_slots < n_seqs) return REDLITE_EINVAL;
+  if (rows > 0) {
+    if (!q || !k || !v || !g || !beta || !out) return REDLITE_EINVAL;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out)) return REDLITE_EINVAL;
+    if (!stride_ok(q_stride, (int64_t)n_k * dk, dtype) || !stride_ok(k_stride, (int64_t)n_k * dk, dtype) ||
+        !stride_ok(v_stride, (int64_t)n_v * dv, dtype) || !stride_ok(out_stride, (int64_t)n_v * dv, dtype))
+      return REDLITE_EINVAL;
+  }
+  return 1;  // there is work
+}
+
+namespace {
+
+constexpr int kStepCols = 32;
+
+template <typename T, int DK>
+__global__ void __launch_bounds__(128) delta_step_kernel(const DeltaArgs a) {
+  constexpr int kRows = DK / 16;  // state rows per thread
+  __shared__ float sk[DK], sq[DK];
+  __shared__ float red[3][4];
+  __shared__ float4 part[2][4][8];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int slices = a.dv / kStepCols;
+  const int slice = blockIdx.x % slices, head = (blockIdx.x / slices) % a.n_v;
+  const int seq = blockIdx.x / (slices * a.n_v);
+  const int kh = head / (a.n_v / a.n_k), col = slice * kStepCols + 4 * (lane & 7), row0 = warp * 4 + (lane >> 3);
+  const int64_t slot = delta_slot(a, seq);
+  T *dst = (T *)a.out + (int64_t)seq * a.out_stride + (int64_t)head * a.dv;
+  if (slot < 0) {
+    if (tid < kStepCols) dst[slice * kStepCols + tid] = from_f32<T>(0.f);
+    return;
+  }
+  const int64_t at = ((slot * a.n_v + head) * DK + row0) * (int64_t)a.dv + col;
+  float4 S[kRows];
+#pragma unroll
+  for (int i = 0; i < kRows; ++i)
+    S[i] = a.state_in ? __ldcs(reinterpret_cast<const float4 *>(a.state_in + at + (int64_t)16 * i * a.dv))
+                      : make_float4(0.f, 0.f, 0.f, 0.f);
+  const float decay = expf(__ldg(a.g + (int64_t)seq * a.n_v + head));
+  const float beta = __ldg(a.beta + (int64_t)seq * a.n_v + head);
+  float v[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    v[j] = to_f32(((const T *)a.v)[(int64_t)seq * a.v_stride + (int64_t)head * a.dv + col + j]);
+  // keys and queries, their norms and product
+  float kk = 0.f, qq = 0.f, qk = 0.f;
+  if (tid < DK) {
+    const float x = to_f32(((const T *)a.k)[(int64_t)seq * a.k_stride + (int64_t)kh * DK + tid]);
+    const float y = to_f32(((const T *)a.q)[(int64_t)seq * a.q_stride + (int64_t)kh * DK + tid]);
+    sk[tid] = x, sq[tid] = y;
+    kk = x * x, qq = y * y, qk = x * y;
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    kk += __shfl_xor_sync(0xffffffffu, kk, o);
+    qq += __shfl_xor_sync(0xffffffffu, qq, o);
+    qk += __shfl_xor_sync(0xffffffffu, qk, o);
+  }
+  if (lane == 0) red[0][warp] = kk, red[1][warp] = qq, red[2][warp] = qk;
+  __syncthreads();
+  kk = (red[0][0] + red[0][1]) + (red[0][2] + red[0][3]);
+  qq = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
+  qk = (red[2][0] + red[2][1]) + (red[2][2] + red[2][3]);
+  float nk = 1.f, nq = 1.f;
+  if (a.qk_eps >= 0.f) nk = 1.f / sqrtf(kk + a.qk_eps), nq = 1.f / sqrtf(qq + a.qk_eps);
+  float4 tk = make_float4(0.f, 0.f, 0.f, 0.f), tq = tk;
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const float x = sk[row0 + 16 * i], y = sq[row0 + 16 * i];
+    tk.x = fmaf(x, S[i].x, tk.x), tk.y = fmaf(x, S[i].y, tk.y), tk.z = fmaf(x, S[i].z, tk.z), tk.w = fmaf(x, S[i].w, tk.w);
+    tq.x = fmaf(y, S[i].x, tq.x), tq.y = fmaf(y, S[i].y, tq.y), tq.z = fmaf(y, S[i].z, tq.z), tq.w = fmaf(y, S[i].w, tq.w);
+  }
+#pragma unroll
+  for (int o = 8; o <= 16; o <<= 1) {
+    tk.x += __shfl_xor_sync(0xffffffffu, tk.x, o), tk.y += __shfl_xor_sync(0xffffffffu, tk.y, o);
+    tk.z += __shfl_xor_sync(0xffffffffu, tk.z, o), tk.w += __shfl_xor_sync(0xffffffffu, tk.w, o);
+    tq.x += __shfl_xor_sync(0xffffffffu, tq.x, o), tq.y += __shfl_xor_sync(0xffffffffu, tq.y, o);
+    tq.z += __shfl_xor_sync(0xffffffffu, tq.z, o), tq.w += __shfl_xor_sync(0xffffffffu, tq.w, o);
+  }
+  if (lane < 8) part[0][warp][lane] = tk, part[1][warp][lane] = tq;
+  __syncthreads();
+  float kS[4] = {0.f, 0.f, 0.f, 0.f}, qS[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const float4 x = part[0][w][lane & 7], y = part[1][w][lane & 7];
+    kS[0] += x.x, kS[1] += x.y, kS[2] += x.z, kS[3] += x.w;
+    qS[0] += y.x, qS[1] += y.y, qS[2] += y.z, qS[3] += y.w;
+  }
+  float d[4], o[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    d[j] = beta * (v[j] - decay * nk * kS[j]);
+    o[j] = a.scale * nq * fmaf(decay, qS[j], nk * qk * d[j]);
+    d[j] *= nk;
+  }
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const float x = sk[row0 + 16 * i];
+    __stcs(reinterpret_cast<float4 *>(a.state_out + at + (int64_t)16 * i * a.dv),
+           make_float4(fmaf(decay, S[i].x, x * d[0]), fmaf(decay, S[i].y, x * d[1]), fmaf(decay, S[i].z, x * d[2]),
+                       fmaf(decay, S[i].w, x * d[3])));
+  }
+  if (tid < 8) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) dst[col + j] = from_f32<T>(o[j]);
+  }
+}
+
+template <typename T>
+cudaError_t launch_step(const DeltaArgs &a, cudaStream_t s) {
+  const unsigned grid = (unsigned)((int64_t)a.n_seqs * a.n_v * (a.dv / kStepCols));
+  if (a.dk == 128) delta_step_kernel<T, 128><<<grid, 128, 0, s>>>(a);
+  else delta_step_kernel<T, 64><<<grid, 128, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+}  // namespace redlite
+
+using namespace redlite;
+
+extern "C" int redlite_delta_step(int32_t dtype, const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                                  const void *v, int64_t v_stride, const float *g, const float *beta, int32_t n_seqs,
+                                  int32_t n_k_heads, int32_t n_v_heads, int32_t dk, int32_t dv, float scale,
+                                  float qk_eps, const float *state_in, float *state_out, const int32_t *slots,
+                                  int64_t n_slots, void *out, int64_t out_stride, int32_t *status, void *stream) {
+  const int rc = delta_check(dtype, q, q_stride, k, k_stride, v, v_stride, g, beta, n_seqs, n_seqs, n_k_heads,
+                             n_v_heads, dk, dv, scale, state_in, state_out, slots, n_slots, out, out_stride);
+  if (rc <= 0) return rc;
+  if ((int64_t)n_seqs * n_v_heads * (dv / kStepCols) >= ((int64_t)1 << 31) - 1) return REDLITE_EUNSUPPORTED;
+  DeltaArgs a = {};
+  a.q = q, a.k = k, a.v = v, a.q_stride = q_stride, a.k_stride = k_stride, a.v_stride = v_stride;
+  a.out_stride = out_stride, a.g = g, a.beta = beta, a.slots = slots;
+  a.n_seqs = n_seqs, a.n_tokens = n_seqs, a.n_k = n_k_heads, a.n_v = n_v_heads, a.dk = dk, a.dv = dv;
+  a.scale = scale, a.qk_eps = qk_eps, a.state_in = state_in, a.state_out = state_out, a.n_slots = n_slots;
+  a.out = out, a.status = status;
+  cudaStream_t s = (cudaStream_t)stream;
+  cudaError_t e;
+  if (dtype == REDLITE_T_F32) e = launch_step<float>(a, s);
+  else if (dtype == REDLITE_T_BF16) e = launch_step<__nv_bfloat16>(a, s);
+  else e = launch_step<__half>(a, s);
+  return e == cudaSuccess ? REDLITE_OK : REDLITE_ECUDA;
+}

@@ -112,3 +112,31 @@ def table(rng, lens, page, spare=0):
 def softmax(z):
     p = np.exp(z - z.max(-1, keepdims=True))
     return p / p.sum(-1, keepdims=True)
+
+
+# -------------------------------------------------------- gated delta rule
+
+
+def delta(q, k, v, g, beta, lens, state, scale, eps):
+    """(out, states, growth) in 64 bits, token by token.  q, k [T, Hk, dk], v [T, Hv, dv], g, beta [T, Hv],
+    state [n, Hv, dk, dv]: the states in front of each sequence.  growth, per sequence and head: the largest
+    norm the state reaches."""
+    hv, r = v.shape[1], v.shape[1] // k.shape[1]
+    if eps >= 0:
+        q = q / np.sqrt((q * q).sum(-1, keepdims=True) + eps)
+        k = k / np.sqrt((k * k).sum(-1, keepdims=True) + eps)
+    q, k = np.repeat(q, r, 1) * scale, np.repeat(k, r, 1)
+    out, S_out = np.zeros(v.shape), state.copy()
+    t = 0
+    big = np.zeros((len(lens), hv))
+    for s, n in enumerate(lens):
+        S = S_out[s]
+        big[s] = np.abs(S).max((1, 2))
+        for _ in range(n):
+            S *= np.exp(g[t])[:, None, None]
+            d = beta[t][:, None] * (v[t] - np.einsum("hkv,hk->hv", S, k[t]))
+            S += k[t][:, :, None] * d[:, None, :]
+            out[t] = np.einsum("hkv,hk->hv", S, q[t])
+            big[s] = np.maximum(big[s], np.abs(S).max((1, 2)))
+            t += 1
+    return out, S_out, big
