@@ -356,8 +356,8 @@ int redlite_proj_gemv(int32_t qtype, const void *W, int64_t rows, int64_t k, con
  *     overlap inputs except where stated.
  *   - Sequences are packed: cu is a device array [n_seqs + 1] of ascending
  *     offsets; sequence s holds rows cu[s] .. cu[s + 1] - 1 (possibly none)
- *     of the n_tokens rows.  Rows in front of cu[0] or behind cu[n_seqs] are
- *     neither read nor written.
+ *     of the n_tokens rows.  Rows in front of cu[0] or behind cu[n_seqs] have
+ *     no effect and are not written.
  *   - status: a device word into which REDLITE_STATUS_* bits are ORed, or
  *     NULL.  Lengths, pages and slots are checked on the device before they
  *     are used; what cannot be served is reported and skipped.
@@ -368,6 +368,25 @@ int redlite_proj_gemv(int32_t qtype, const void *W, int64_t rows, int64_t k, con
  *   - REDLITE_EINVAL: a null pointer, a size, stride or alignment out of
  *     range; REDLITE_EUNSUPPORTED: a head size or page size the kernels do
  *     not take; REDLITE_ENOMEM: workspace too small. */
+
+/* Causal attention over packed prompts with grouped heads:
+ *   out[i, h] = sum_j softmax_j(scale * q[i, h] . k[j, kh]) v[j, kh]
+ * kh = h / (n_heads / n_kv_heads); query i of sequence s (nq queries, nk
+ * keys) sees keys 0 .. i + nk - nq of that sequence (the last query sees
+ * all); a query that sees none gives zeros.  What a masked place holds (NaN
+ * and infinities included) has no effect.
+ *   dtype       REDLITE_T_BF16 or REDLITE_T_F16 (else EUNSUPPORTED: the
+ *               products run on the tensor cores in the inputs' own type)
+ *   q, out      device [n_q rows, n_heads * head_dim]
+ *   k, v        device [n_k rows, n_kv_heads * head_dim]
+ *   cu_q, cu_k  device [n_seqs + 1] each; a sequence whose offsets do not
+ *               ascend within the rows is reported, its outputs not written
+ *   head_dim    128 or 256;  scale > 0, finite
+ * Probabilities are rounded to dtype in front of the second product. */
+int redlite_attn_prefill(int32_t dtype, const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                         const void *v, int64_t v_stride, const int32_t *cu_q, const int32_t *cu_k, int32_t n_seqs,
+                         int32_t n_q, int32_t n_k, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim, float scale,
+                         void *out, int64_t out_stride, int32_t *status, void *stream);
 
 /* The paged key/value cache in 4 bits.  A page holds page_size tokens (a
  * multiple of 16, up to 4096) of all key/value heads, redlite_kv4_page_bytes
@@ -436,8 +455,8 @@ int redlite_kv4_decode(int32_t dtype, const void *q, int64_t q_stride, int32_t n
  * redlite_delta_prefill runs packed sequences of any lengths in chunks of 64
  * tokens (with n_tokens = 0 it copies the states); workspace 256-byte
  * aligned.  A cu that does not ascend within 0 .. n_tokens is reported; the
- * sequences it breaks are skipped, their states not written.  redlite_delta_step runs one token per
- * sequence: row s is sequence s. */
+ * sequences it breaks are skipped, their states not written.
+ * redlite_delta_step runs one token per sequence: row s is sequence s. */
 size_t redlite_delta_workspace_bytes(int32_t n_tokens, int32_t n_seqs, int32_t n_k_heads, int32_t n_v_heads, int32_t dk,
                                      int32_t dv);
 int redlite_delta_prefill(int32_t dtype, const void *q, int64_t q_stride, const void *k, int64_t k_stride,

@@ -100,6 +100,9 @@ EXPORTS = {
     "redlite_proj_matrix_bytes": (ctypes.c_size_t, [ctypes.c_int32, ctypes.c_int64, ctypes.c_int64]),
     "redlite_proj_gemv": (ctypes.c_int, [ctypes.c_int32, _c_void_p, ctypes.c_int64, ctypes.c_int64, _c_void_p,
                                          ctypes.c_int32, _c_void_p, _c_void_p]),
+    "redlite_attn_prefill": (ctypes.c_int, [_i32, _c_void_p, _i64, _c_void_p, _i64, _c_void_p, _i64, _c_void_p,
+                                            _c_void_p, _i32, _i32, _i32, _i32, _i32, _i32, ctypes.c_float, _c_void_p,
+                                            _i64, _c_void_p, _c_void_p]),
     "redlite_kv4_page_bytes": (ctypes.c_size_t, [_i32] * 3),
     "redlite_kv4_append": (ctypes.c_int, [_i32, _c_void_p, _c_void_p, _i64, _i64, _c_void_p, _c_void_p, _i32, _i32, _i32,
                                           _i32, _i32, _c_void_p, _i32, _i64, _c_void_p, _c_void_p, _c_void_p]),
@@ -328,6 +331,20 @@ def _mixer_ok(acts, dense) -> bool:
 def _on(device, stream):
     s = torch.cuda.current_stream(device) if stream is None else stream
     return ctypes.c_void_p(s.cuda_stream)
+
+
+def redlite_attn_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.Tensor, cu_k: torch.Tensor,
+                         out: torch.Tensor, scale: float, status: Optional[torch.Tensor] = None, stream=None) -> int:
+    """Causal attention over packed prompts: q, out [n_q, n_heads, head_dim]; k, v [n_k, n_kv_heads, head_dim]."""
+    n = cu_q.numel() - 1
+    if (n < 0 or not _mixer_ok((q, k, v, out), ((cu_q, torch.int32), (cu_k, torch.int32), (status, torch.int32)))
+            or q.shape != out.shape or k.shape != v.shape or q.shape[2] != k.shape[2] or cu_k.numel() != n + 1):
+        return REDLITE_EINVAL
+    with torch.cuda.device(q.device):
+        return lib().redlite_attn_prefill(
+            _DTYPES[q.dtype], _ptr(q), _row_stride(q), _ptr(k), _row_stride(k), _ptr(v), _row_stride(v), _ptr(cu_q),
+            _ptr(cu_k), n, q.shape[0], k.shape[0], q.shape[1], k.shape[1], q.shape[2], float(scale), _ptr(out),
+            _row_stride(out), _ptr(status), _on(q.device, stream))
 
 
 def redlite_kv4_page_bytes(n_kv_heads: int, head_dim: int, page_size: int) -> int:

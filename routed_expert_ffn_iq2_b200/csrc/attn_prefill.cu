@@ -1,0 +1,523 @@
+// attn_prefill.cu -- causal attention over packed prompts with grouped heads
+// (redlite_attn_prefill).  ("Red Lite dev16 -- complete full-attention
+// parity", section "Pinned full-attention graph": 16 query heads on 2
+// key/value heads of 256.)
+//
+//   O = softmax(scale Q K^T) V, one pass over the keys with a running
+//   reference m and sum l per row: p = 2^(s - m), l += p, O += p V; when a
+//   score passes m by more than 2^8 (and at a row's first keys), l and O are
+//   rescaled by 2^(m - m') -- rare, and exact otherwise.
+//
+// Both products run on the tensor cores (tcgen05, fp32 accumulators in tensor
+// memory), 4 D flops per visible pair, which is the bound: a tile of 128 rows
+// by 128 keys takes 2 x 128 x 128 x D multiply-adds against 128 x 128
+// exponentials.  One block per 128 rows (D = 256) or 2 x 128 rows (D = 128);
+// the rows of a tile are tokens x the query heads that share a key/value head
+// (the largest power of two G of them), so keys are read once for G heads and
+// a prompt of a few tokens still fills its tile.
+//   warp 0      one thread: TMA loads of Q (once) and of K and V in a ring of
+//               five 32 KB stages (128B-swizzled boxes)
+//   warp 1      one thread: issues the products.  Scores of step i + 1 are
+//               issued in front of the second product of step i, so the
+//               tensor cores work while the softmax does
+//   warp 2      tensor memory allocation
+//   warps 4 ..  softmax: thread = row.  Scores come out of tensor memory,
+//               probabilities go back over them in the inputs' type (that
+//               rounding, 2^-8 or 2^-11 of each p at most, is what the product's type
+//               asks for; l sums the unrounded p)
+// Steps: D = 256, one row tile, two score buffers used in turn; D = 128, two
+// row tiles with a buffer and a softmax group each, in turn.
+//
+// A zero probability times a NaN or an infinity in V is a NaN that a masked
+// key must not cause: a row whose result is not finite is computed again by
+// its warp from the keys it sees alone.
+#include <cuda.h>
+
+#include <type_traits>
+
+#include "mixer.cuh"
+
+namespace redlite {
+namespace {
+
+struct AttnArgs {
+  const void *q, *k, *v;
+  void *out;
+  int64_t q_stride, k_stride, v_stride, out_stride;
+  const int32_t *cu_q, *cu_k;
+  int n_seqs, n_q, n_k, n_heads, n_kv, group, log_group;
+  float scale_log2;
+  int32_t *status;
+};
+
+constexpr int kKeys = 128;          // keys per step
+constexpr int kStageBytes = 32768;  // 128 keys x 128 values (K), or 64 x 256 / 128 x 128 (V)
+constexpr int kRing = 5;
+constexpr int kQBytes = 65536;
+constexpr float kLazy = 8.f;
+
+template <int D>
+struct Shape {
+  static constexpr int NQ = D == 128 ? 2 : 1;   // row tiles per block
+  static constexpr int kSub = D / 128;          // stages per K or V tile
+  static constexpr int kWarps = 4 + 4 * NQ;
+  static constexpr uint32_t kO = 256;           // first accumulator column of O (scores: 0 and 128)
+};
+
+struct Bars {
+  uint64_t q_full, full[kRing], empty[kRing], s_full[2], p_full[2], o_full[2];
+  uint32_t tmem;
+  int dead;
+};
+
+constexpr int kSmem = kQBytes + kRing * kStageBytes + (int)sizeof(Bars) + 1024;
+static_assert(kSmem <= 227 * 1024, "shared memory of a block");
+
+__device__ __forceinline__ void tma_load3(void *dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          ptx::smem_u32(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(ptx::smem_u32(bar))
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t *v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
+        "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
+        "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+      : "r"(taddr));
+}
+
+// Descriptor of a tile whose rows run along K and whose 64-element row pieces
+// (128 bytes, swizzled) run along N: `lead` bytes between 64-column pieces,
+// 1024 between groups of 8 rows.
+__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t addr, uint32_t lead) {
+  return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)((lead >> 4) & 0x3FFFu) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+// Bounded wait; after one that gave up every later one returns at once.
+__device__ __forceinline__ bool wait(Bars *b, uint64_t *bar, uint32_t parity, int32_t *status) {
+  if (ptx::mbar_try_wait(bar, parity)) return true;
+  if (*(volatile int *)&b->dead) return false;
+  if (ptx::mbar_wait_suspend(bar, parity)) return true;
+  *(volatile int *)&b->dead = 1;
+  set_status(status, REDLITE_STATUS_TIMEOUT);
+  return false;
+}
+
+// One row by one warp, from the keys it sees alone, fp32.
+template <typename T, int D>
+__device__ __noinline__ void row_again(const AttnArgs &a, int64_t q_row, int head, int64_t k_row0, int lim) {
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31, kh = head / (a.n_heads / a.n_kv);
+  float q[E], o[E], m = -INFINITY, l = 0.f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    q[e] = to_f32(((const T *)a.q)[q_row * a.q_stride + (int64_t)head * D + lane + 32 * e]);
+    o[e] = 0.f;
+  }
+  for (int j = 0; j < lim; ++j) {
+    const T *k = (const T *)a.k + (k_row0 + j) * a.k_stride + (int64_t)kh * D;
+    const T *v = (const T *)a.v + (k_row0 + j) * a.v_stride + (int64_t)kh * D;
+    float s = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) s = fmaf(q[e], to_f32(k[lane + 32 * e]), s);
+#pragma unroll
+    for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
+    s *= a.scale_log2;
+    const float mn = s > m ? s : m;  // a NaN leaves m and makes p a NaN
+    const float f = m == -INFINITY ? 0.f : ex2(m - mn), p = s == -INFINITY ? 0.f : ex2(s - mn);
+    l = l * f + p;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = o[e] * f + p * to_f32(v[lane + 32 * e]);
+    m = mn;
+  }
+  const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+#pragma unroll
+  for (int e = 0; e < E; ++e)
+    ((T *)a.out)[q_row * a.out_stride + (int64_t)head * D + lane + 32 * e] = from_f32<T>(o[e] * inv);
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(32 * Shape<D>::kWarps, 1)
+    attn_prefill_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                        const __grid_constant__ CUtensorMap mv, const AttnArgs a) {
+  using Sh = Shape<D>;
+  constexpr int NQ = Sh::NQ, kSub = Sh::kSub;
+  constexpr bool kBf = sizeof(T) == 2 && std::is_same<T, __nv_bfloat16>::value;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = smem_raw + ((1024 - (ptx::smem_u32(smem_raw) & 1023)) & 1023);
+  uint8_t *sq = smem, *ring = smem + kQBytes;
+  Bars *b = reinterpret_cast<Bars *>(ring + kRing * kStageBytes);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (blockIdx.x == 0)
+    for (int s = threadIdx.x; s < a.n_seqs; s += blockDim.x) {
+      const int b0 = __ldg(a.cu_q + s), e0 = __ldg(a.cu_q + s + 1), b1 = __ldg(a.cu_k + s), e1 = __ldg(a.cu_k + s + 1);
+      if (b0 < 0 || e0 < b0 || e0 > a.n_q || b1 < 0 || e1 < b1 || e1 > a.n_k) set_status(a.status, REDLITE_STATUS_BAD_LENGTH);
+    }
+  // ---- which rows: the last tiles of the last sequences first (most keys)
+  const int tile_tok = kKeys >> a.log_group, block_tok = NQ * tile_tok;
+  const int hb = blockIdx.x % (a.n_heads >> a.log_group);
+  const int64_t slot = (gridDim.x - 1 - blockIdx.x) / (a.n_heads >> a.log_group);
+  int lo = 0, hi = a.n_seqs;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if ((int64_t)(__ldg(a.cu_q + mid) / block_tok) + mid <= slot) lo = mid;
+    else hi = mid;
+  }
+  const int q0 = __ldg(a.cu_q + lo), q1 = __ldg(a.cu_q + lo + 1), k0 = __ldg(a.cu_k + lo), k1 = __ldg(a.cu_k + lo + 1);
+  const bool valid = q0 >= 0 && q1 >= q0 && q1 <= a.n_q && k0 >= 0 && k1 >= k0 && k1 <= a.n_k;
+  if (!valid) return;
+  const int64_t t0l = (slot - ((int64_t)(q0 / block_tok) + lo)) * block_tok;
+  const int q_len = q1 - q0, k_len = k1 - k0;
+  if (t0l < 0 || t0l >= q_len) return;
+  const int t0 = (int)t0l;
+  const int shift = k_len - q_len;  // query t sees keys 0 .. t + shift
+  const int lim_max = max(0, min(q_len, t0 + block_tok) + shift);
+  const int n_tiles = (lim_max + kKeys - 1) / kKeys;
+  const int head0 = hb << a.log_group, kh = head0 / (a.n_heads / a.n_kv);
+
+  if (threadIdx.x == 0) {
+    ptx::mbar_init(&b->q_full, 1);
+    for (int i = 0; i < kRing; ++i) ptx::mbar_init(b->full + i, 1), ptx::mbar_init(b->empty + i, 1);
+    for (int i = 0; i < 2; ++i)
+      ptx::mbar_init(b->s_full + i, 1), ptx::mbar_init(b->p_full + i, 128), ptx::mbar_init(b->o_full + i, 1);
+    b->dead = 0;
+    ptx::mbar_fence_init();
+  }
+  if (warp == 2) {
+    ptx::tmem_alloc(&b->tmem, 512);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = b->tmem;
+
+  if (warp == 0 && lane == 0 && n_tiles > 0) {
+    // ================================================================ loads
+    ptx::mbar_expect_tx(&b->q_full, kQBytes);
+    for (int t = 0; t < NQ; ++t)
+      for (int d = 0; d < D / 64; ++d)
+        tma_load3(sq + (t * (D / 64) + d) * 16384, &mq, 64 * d, head0, q0 + t0 + t * tile_tok, &b->q_full);
+    int st = 0;
+    uint32_t ph = 1;  // parity with which an empty stage is waited for (the first round passes)
+    auto next = [&]() -> uint8_t * {  // null once a wait gave up: no copy is started any more
+      if (!wait(b, b->empty + st, ph, a.status)) return nullptr;
+      ptx::mbar_expect_tx(b->full + st, kStageBytes);
+      return ring + st * kStageBytes;
+    };
+    auto step = [&]() {
+      if (++st == kRing) st = 0, ph ^= 1;
+    };
+    auto load_k = [&](int i) {
+      for (int h = 0; h < kSub; ++h) {
+        uint8_t *dst = next();
+        if (!dst) return;
+        for (int d = 0; d < 2; ++d) tma_load3(dst + d * 16384, &mk, 128 * h + 64 * d, kh, k0 + i * kKeys, b->full + st);
+        step();
+      }
+    };
+    auto load_v = [&](int i) {
+      constexpr int kRows = kKeys / kSub;
+      for (int h = 0; h < kSub; ++h) {
+        uint8_t *dst = next();
+        if (!dst) return;
+        for (int d = 0; d < D / 64; ++d)
+          tma_load3(dst + d * kRows * 128, &mv, 64 * d, kh, k0 + i * kKeys + h * kRows, b->full + st);
+        step();
+      }
+    };
+    load_k(0);
+    for (int i = 0; i < n_tiles && !*(volatile int *)&b->dead; ++i) {
+      if (NQ == 1) {
+        if (i + 1 < n_tiles) load_k(i + 1);
+        load_v(i);
+      } else {
+        load_v(i);
+        if (i + 1 < n_tiles) load_k(i + 1);
+      }
+    }
+  } else if (warp == 1 && lane == 0 && n_tiles > 0) {
+    // ============================================================= products
+    constexpr uint32_t fmt = kBf ? ((1u << 7) | (1u << 10)) : 0u;
+    constexpr uint32_t id_s = (1u << 4) | fmt | ((kKeys >> 3) << 17) | ((128u >> 4) << 24);
+    constexpr uint32_t id_o = (1u << 4) | fmt | (1u << 16) | ((uint32_t)(D >> 3) << 17) | ((128u >> 4) << 24);
+    const uint32_t q_addr = ptx::smem_u32(sq), r_addr = ptx::smem_u32(ring);
+    int st = 0;         // ring stage of the next K or V tile
+    uint32_t ph = 0;
+    auto stage_wait = [&](int s, uint32_t p) { wait(b, b->full + s, p, a.status); };
+    // scores of one row tile: K tile in stages s ..
+    auto scores = [&](int row_tile, int buf, int s, uint32_t p, bool release) {
+      for (int h = 0; h < kSub; ++h) {
+        stage_wait(s, p);
+        ptx::tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          const uint64_t da = ptx::sdesc_k_sw128(q_addr + (row_tile * (D / 64) + 2 * h + kk / 4) * 16384 + (kk % 4) * 32);
+          const uint64_t db = ptx::sdesc_k_sw128(r_addr + s * kStageBytes + (kk / 4) * 16384 + (kk % 4) * 32);
+          ptx::umma_bf16(tmem + 128 * buf, da, db, id_s, h > 0 || kk > 0);
+        }
+        if (release) ptx::umma_commit(b->empty + s);
+        if (++s == kRing) s = 0, p ^= 1;
+      }
+      ptx::umma_commit(b->s_full + buf);
+    };
+    auto outputs = [&](int buf, int acc, int s, uint32_t p, bool first, bool release) {
+      constexpr int kRows = kKeys / kSub;
+      for (int h = 0; h < kSub; ++h) {
+        stage_wait(s, p);
+        ptx::tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < kRows / 16; ++kk) {
+          const uint64_t dv = sdesc_mn_sw128(r_addr + s * kStageBytes + kk * 2048, kRows * 128);
+          ptx::umma_bf16_ts(tmem + Sh::kO + 128 * acc, tmem + 128 * buf + (h * kRows + kk * 16) / 2, dv, id_o,
+                            !first || h > 0 || kk > 0);
+        }
+        if (release) ptx::umma_commit(b->empty + s);
+        if (++s == kRing) s = 0, p ^= 1;
+      }
+      ptx::umma_commit(b->o_full + acc);
+    };
+    auto skip = [&](int &s, uint32_t &p) {
+      s += kSub;
+      if (s >= kRing) s -= kRing, p ^= 1;
+    };
+    wait(b, &b->q_full, 0, a.status);
+    if (NQ == 1) {
+      scores(0, 0, st, ph, true);
+      skip(st, ph);
+      for (int i = 0; i < n_tiles && !*(volatile int *)&b->dead; ++i) {
+        if (i + 1 < n_tiles) {
+          scores(0, (i + 1) & 1, st, ph, true);
+          skip(st, ph);
+        }
+        wait(b, b->p_full + (i & 1), (i >> 1) & 1, a.status);
+        outputs(i & 1, 0, st, ph, i == 0, true);
+        skip(st, ph);
+      }
+    } else {
+      scores(0, 0, st, ph, false);
+      scores(1, 1, st, ph, true);
+      skip(st, ph);
+      for (int i = 0; i < n_tiles && !*(volatile int *)&b->dead; ++i) {
+        int s2 = st;  // V tile of this step, then K tile of the next
+        uint32_t p2 = ph;
+        skip(s2, p2);
+        for (int t = 0; t < 2; ++t) {
+          wait(b, b->p_full + t, i & 1, a.status);
+          outputs(t, t, st, ph, i == 0, t == 1);
+          if (i + 1 < n_tiles) scores(t, t, s2, p2, t == 1);
+        }
+        skip(st, ph);
+        skip(st, ph);
+      }
+    }
+  } else if (warp >= 4) {
+    // ============================================================== softmax
+    const int wg = (warp - 4) >> 2, row = 32 * (warp & 3) + lane;
+    const int tok = t0 + wg * tile_tok + (row >> a.log_group), head = head0 + (row & (a.group - 1));
+    const bool mine = tok < q_len;
+    const int lim = mine ? max(0, tok + shift + 1) : 0;
+    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t t_o = tmem + lanes + Sh::kO + 128 * wg;
+    float m = -INFINITY, l = 0.f;
+    for (int i = 0; i < n_tiles && !*(volatile int *)&b->dead; ++i) {
+      const int buf = NQ == 1 ? (i & 1) : wg;
+      const uint32_t t_s = tmem + lanes + 128 * buf;
+      wait(b, b->s_full + buf, NQ == 1 ? (i >> 1) & 1 : i & 1, a.status);
+      __syncwarp();
+      ptx::tc_fence_after();
+      uint32_t s[kKeys];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) tmem_ld32(t_s + 32 * j, s + 32 * j);
+      ptx::tmem_wait_ld();
+      const int left = lim - i * kKeys;  // keys of this tile that the row sees
+      if (__any_sync(0xffffffffu, left < kKeys)) {
+#pragma unroll
+        for (int j = 0; j < kKeys; ++j) s[j] = j < left ? s[j] : 0xff800000u;
+      }
+      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int j = 0; j < kKeys; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(s[j]));
+      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
+      if (__any_sync(0xffffffffu, top > m + kLazy || (m == -INFINITY && top > -INFINITY))) {
+        const float mn = fmaxf(m, top);
+        const float f = m == -INFINITY ? 0.f : ex2(m - mn);
+        m = mn;
+        l *= f;
+        if (i > 0) {
+          // the product of the step in front has to be in
+          wait(b, b->o_full + (NQ == 1 ? 0 : wg), (i - 1) & 1, a.status);
+          __syncwarp();
+          ptx::tc_fence_after();
+#pragma unroll 1
+          for (int d = 0; d < D; d += 32) {
+            uint32_t o[32];
+            tmem_ld32(t_o + d, o);
+            ptx::tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+            ptx::tmem_st32x32b_x32(t_o + d, o);
+          }
+        }
+      }
+      const float neg = m == -INFINITY ? 0.f : -m;
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t p[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          const float x = ex2(fmaf(__uint_as_float(s[64 * h + 2 * j]), a.scale_log2, neg));
+          const float y = ex2(fmaf(__uint_as_float(s[64 * h + 2 * j + 1]), a.scale_log2, neg));
+          sum[(2 * j) & 3] += x, sum[(2 * j + 1) & 3] += y;
+          p[j] = kBf ? pack_bf16(x, y) : pack_f16(x, y);
+        }
+        ptx::tmem_st32x32b_x32(t_s + 32 * h, p);
+      }
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      ptx::tmem_wait_st();
+      ptx::tc_fence_before();
+      ptx::mbar_arrive(b->p_full + buf);
+    }
+    // ---- rows out
+    T *dst = (T *)a.out + (int64_t)(q0 + tok) * a.out_stride + (int64_t)head * D;
+    bool odd = false;
+    if (n_tiles > 0) {
+      wait(b, b->o_full + (NQ == 1 ? 0 : wg), (n_tiles - 1) & 1, a.status);
+      __syncwarp();
+      ptx::tc_fence_after();
+    }
+    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+#pragma unroll 1
+    for (int d = 0; d < D; d += 32) {
+      uint32_t o[32];
+      if (n_tiles > 0) {
+        tmem_ld32(t_o + d, o);
+        ptx::tmem_wait_ld();
+      } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) o[j] = 0u;
+      }
+      float chk = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(o[8 * j + e]) * inv, chk = fmaf(x[e], 0.f, chk);
+        if (mine) store8<T>(dst + d + 8 * j, x);
+      }
+      odd = odd || !(chk == 0.f);
+    }
+    ptx::tc_fence_before();
+    uint32_t again = __ballot_sync(0xffffffffu, odd && mine);
+    while (again) {
+      const int src = __ffs(again) - 1;
+      again &= again - 1;
+      __syncwarp();
+      row_again<T, D>(a, q0 + __shfl_sync(0xffffffffu, tok, src), __shfl_sync(0xffffffffu, head, src), k0,
+                      __shfl_sync(0xffffffffu, lim, src));
+    }
+  }
+  __syncthreads();
+  ptx::tc_fence_after();
+  if (warp == 2) ptx::tmem_dealloc(tmem, 512);
+}
+
+typedef CUresult (*EncodeTiled)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled() {
+  static EncodeTiled fn = nullptr;
+  if (!fn) {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r) == cudaSuccess &&
+        r == cudaDriverEntryPointSuccess)
+      fn = (EncodeTiled)p;
+  }
+  return fn;
+}
+
+// [tokens, heads, D] rows of 2-byte elements; boxes of 64 x heads x tokens.
+bool make_map(CUtensorMap *m, int32_t dtype, const void *p, int64_t stride, int64_t tokens, int heads, int D,
+              int box_heads, int box_tokens) {
+  EncodeTiled enc = encode_tiled();
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)tokens};
+  const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)stride * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_tokens}, unit[3] = {1, 1, 1};
+  return enc(m, dtype == REDLITE_T_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+             const_cast<void *>(p), dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+         CUDA_SUCCESS;
+}
+
+template <typename T, int D>
+int launch_attn(const AttnArgs &a, int32_t dtype, cudaStream_t s) {
+  CUtensorMap mq, mk, mv;
+  const int tile_tok = kKeys >> a.log_group;
+  constexpr int v_rows = kKeys / Shape<D>::kSub;
+  // without keys no K or V box is loaded; the maps still need an address
+  const void *k = a.n_k > 0 ? a.k : a.q, *v = a.n_k > 0 ? a.v : a.q;
+  const int64_t ks = a.n_k > 0 ? a.k_stride : a.q_stride, vs = a.n_k > 0 ? a.v_stride : a.q_stride;
+  const int hk = a.n_k > 0 ? a.n_kv : a.n_heads;
+  const int64_t nk = a.n_k > 0 ? a.n_k : a.n_q;
+  if (!make_map(&mq, dtype, a.q, a.q_stride, a.n_q, a.n_heads, D, a.group, tile_tok) ||
+      !make_map(&mk, dtype, k, ks, nk, hk, D, 1, kKeys) || !make_map(&mv, dtype, v, vs, nk, hk, D, 1, v_rows))
+    return REDLITE_ECUDA;
+  if (cudaFuncSetAttribute(attn_prefill_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
+    return REDLITE_ECUDA;
+  const int block_tok = Shape<D>::NQ * tile_tok;
+  const int64_t grid = ((int64_t)a.n_q / block_tok + a.n_seqs) * (a.n_heads >> a.log_group);
+  if (grid >= ((int64_t)1 << 31) - 1) return REDLITE_EUNSUPPORTED;
+  attn_prefill_kernel<T, D><<<(unsigned)grid, 32 * Shape<D>::kWarps, kSmem, s>>>(mq, mk, mv, a);
+  return cudaGetLastError() == cudaSuccess ? REDLITE_OK : REDLITE_ECUDA;
+}
+
+}  // namespace
+}  // namespace redlite
+
+using namespace redlite;
+
+extern "C" int redlite_attn_prefill(int32_t dtype, const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                                    const void *v, int64_t v_stride, const int32_t *cu_q, const int32_t *cu_k,
+                                    int32_t n_seqs, int32_t n_q, int32_t n_k, int32_t n_heads, int32_t n_kv_heads,
+                                    int32_t head_dim, float scale, void *out, int64_t out_stride, int32_t *status,
+                                    void *stream) {
+  if (!dtype_ok(dtype) || n_seqs < 0 || n_q < 0 || n_k < 0 || n_heads < 1 || n_heads > 4096 || n_kv_heads < 1 ||
+      n_heads % n_kv_heads)
+    return REDLITE_EINVAL;
+  if (dtype == REDLITE_T_F32 || (head_dim != 128 && head_dim != 256)) return REDLITE_EUNSUPPORTED;
+  if (!(scale > 0.f) || !(scale < INFINITY)) return REDLITE_EINVAL;
+  if (n_seqs == 0 || n_q == 0) return REDLITE_OK;
+  if (!q || !out || !cu_q || !cu_k || (n_k > 0 && (!k || !v))) return REDLITE_EINVAL;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out)) return REDLITE_EINVAL;
+  const int64_t row_q = (int64_t)n_heads * head_dim, row_k = (int64_t)n_kv_heads * head_dim;
+  if (!stride_ok(q_stride, row_q, dtype) || !stride_ok(out_stride, row_q, dtype)) return REDLITE_EINVAL;
+  if (n_k > 0 && (!stride_ok(k_stride, row_k, dtype) || !stride_ok(v_stride, row_k, dtype))) return REDLITE_EINVAL;
+  if (q_stride >= (int64_t)1 << 38 || k_stride >= (int64_t)1 << 38 || v_stride >= (int64_t)1 << 38)
+    return REDLITE_EUNSUPPORTED;
+  AttnArgs a;
+  a.q = q, a.k = k, a.v = v, a.out = out;
+  a.q_stride = q_stride, a.k_stride = k_stride, a.v_stride = v_stride, a.out_stride = out_stride;
+  a.cu_q = cu_q, a.cu_k = cu_k, a.n_seqs = n_seqs, a.n_q = n_q, a.n_k = n_k, a.n_heads = n_heads, a.n_kv = n_kv_heads;
+  const int ratio = n_heads / n_kv_heads;
+  a.log_group = 0;
+  while (a.log_group < 6 && ratio % (2 << a.log_group) == 0) ++a.log_group;
+  a.group = 1 << a.log_group;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.status = status;
+  cudaStream_t s = (cudaStream_t)stream;
+  if (dtype == REDLITE_T_BF16)
+    return head_dim == 256 ? launch_attn<__nv_bfloat16, 256>(a, dtype, s) : launch_attn<__nv_bfloat16, 128>(a, dtype, s);
+  return head_dim == 256 ? launch_attn<__half, 256>(a, dtype, s) : launch_attn<__half, 128>(a, dtype, s);
+}
