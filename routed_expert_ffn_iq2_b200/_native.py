@@ -2,7 +2,8 @@
 with the same names.  Argument marshalling only -- torch supplies device
 memory and the current stream; every step of the layer runs in the
 library's CUDA kernels.  There is no fallback: if the library is missing
-or fails to load, every call raises."""
+or fails to load, every call raises.  The token mixers go through _marshal.so
+(csrc/marshal.cpp), the same marshalling in C++ on the same C ABI."""
 
 from __future__ import annotations
 
@@ -302,98 +303,53 @@ def redlite_proj_gemv(qtype: int, W: torch.Tensor, rows: int, k: int, x: torch.T
 # (slices of a joint projection); sizes and the element type are read off the
 # tensors.  A call runs on the tensors' device, on `stream` or that device's
 # current stream; `status` is an optional int32 tensor of one element.
+# Tensors that do not fit together give REDLITE_EINVAL.  The checks and the
+# marshalling are native (csrc/marshal.cpp): a single-token call takes less
+# time on the device than the same checks take in Python.
 
-_DTYPES = {torch.float32: REDLITE_T_F32, torch.bfloat16: REDLITE_T_BF16, torch.float16: REDLITE_T_F16}
-
-
-def _heads_ok(t: torch.Tensor) -> bool:
-    """[rows, heads, head_dim] on a GPU with dense heads; only the row stride is free."""
-    return (t.is_cuda and t.dim() == 3 and t.dtype in _DTYPES and (t.shape[2] <= 1 or t.stride(2) == 1)
-            and (t.shape[1] <= 1 or t.stride(1) == t.shape[2]))
+_marshal_mod = None
 
 
-def _row_stride(t: torch.Tensor) -> int:
-    # the stride of a dimension of one element says nothing
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+def _marshal():
+    """The native argument marshaller (raises if it is not built)."""
+    global _marshal_mod
+    if _marshal_mod is None:
+        lib()
+        from . import _marshal as mod  # beside libredlite_moe.so, built with it
+
+        _marshal_mod = mod
+    return _marshal_mod
 
 
-def _dense(t: Optional[torch.Tensor], dtype: torch.dtype, device) -> bool:
-    return t is None or (t.dtype == dtype and t.is_contiguous() and t.device == device)
-
-
-def _mixer_ok(acts, dense) -> bool:
-    """Activations of one type and device; (tensor, dtype) pairs that are dense and beside them."""
-    d, t = acts[0].device, acts[0].dtype
-    return (all(_heads_ok(x) and x.device == d and x.dtype == t for x in acts)
-            and all(_dense(x, dt, d) for x, dt in dense))
-
-
-def _on(device, stream):
-    s = torch.cuda.current_stream(device) if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+def _handle(stream):
+    return None if stream is None else stream.cuda_stream
 
 
 def redlite_attn_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.Tensor, cu_k: torch.Tensor,
                          out: torch.Tensor, scale: float, status: Optional[torch.Tensor] = None, stream=None) -> int:
     """Causal attention over packed prompts: q, out [n_q, n_heads, head_dim]; k, v [n_k, n_kv_heads, head_dim]."""
-    n = cu_q.numel() - 1
-    if (n < 0 or not _mixer_ok((q, k, v, out), ((cu_q, torch.int32), (cu_k, torch.int32), (status, torch.int32)))
-            or q.shape != out.shape or k.shape != v.shape or q.shape[2] != k.shape[2] or cu_k.numel() != n + 1):
-        return REDLITE_EINVAL
-    with torch.cuda.device(q.device):
-        return lib().redlite_attn_prefill(
-            _DTYPES[q.dtype], _ptr(q), _row_stride(q), _ptr(k), _row_stride(k), _ptr(v), _row_stride(v), _ptr(cu_q),
-            _ptr(cu_k), n, q.shape[0], k.shape[0], q.shape[1], k.shape[1], q.shape[2], float(scale), _ptr(out),
-            _row_stride(out), _ptr(status), _on(q.device, stream))
+    return (_marshal_mod or _marshal()).attn_prefill(q, k, v, cu_q, cu_k, out, scale, status, _handle(stream))
 
 
 def redlite_kv4_page_bytes(n_kv_heads: int, head_dim: int, page_size: int) -> int:
     return int(lib().redlite_kv4_page_bytes(n_kv_heads, head_dim, page_size))
 
 
-def _kv4_pages(cache: torch.Tensor, n_kv_heads: int, head_dim: int, page_size: int) -> int:
-    """Pages a cache tensor holds, or -1 if it is not one of whole pages."""
-    b = redlite_kv4_page_bytes(n_kv_heads, head_dim, page_size)
-    n = cache.numel() * cache.element_size()
-    return n // b if b and n % b == 0 else -1
-
-
 def redlite_kv4_append(k: torch.Tensor, v: torch.Tensor, cu_tokens: torch.Tensor, start: torch.Tensor,
                        block_table: torch.Tensor, cache: torch.Tensor, page_size: int,
                        status: Optional[torch.Tensor] = None, stream=None) -> int:
-    """Store k, v [n_tokens, n_kv_heads, head_dim] as tokens start[s].. of each sequence in the 4-bit cache."""
-    n = start.numel()
-    if (not _mixer_ok((k, v), ((cu_tokens, torch.int32), (start, torch.int32), (block_table, torch.int32),
-                               (cache, torch.uint8), (status, torch.int32)))
-            or k.shape != v.shape or cu_tokens.numel() != n + 1 or block_table.dim() != 2 or block_table.shape[0] != n):
-        return REDLITE_EINVAL
-    T, H, D = k.shape
-    pages = _kv4_pages(cache, H, D, page_size)
-    if pages < 0:
-        return REDLITE_EUNSUPPORTED if redlite_kv4_page_bytes(H, D, page_size) == 0 else REDLITE_EINVAL
-    with torch.cuda.device(k.device):
-        return lib().redlite_kv4_append(_DTYPES[k.dtype], _ptr(k), _ptr(v), _row_stride(k), _row_stride(v),
-                                        _ptr(cu_tokens), _ptr(start), n, T, H, D, page_size, _ptr(block_table),
-                                        block_table.shape[1], pages, _ptr(cache), _ptr(status), _on(k.device, stream))
+    """Store k, v [n_tokens, n_kv_heads, head_dim] as tokens start[s].. of each sequence in the 4-bit cache
+    (uint8, whole pages of redlite_kv4_page_bytes)."""
+    return (_marshal_mod or _marshal()).kv4_append(k, v, cu_tokens, start, block_table, cache, page_size, status,
+                                                   _handle(stream))
 
 
 def redlite_kv4_load(cache: torch.Tensor, page_size: int, block_table: torch.Tensor, cu_tokens: torch.Tensor,
                      start: torch.Tensor, k: torch.Tensor, v: torch.Tensor, status: Optional[torch.Tensor] = None,
                      stream=None) -> int:
     """The values the cache stands for, into k and v [n_tokens, n_kv_heads, head_dim]."""
-    n = start.numel()
-    if (not _mixer_ok((k, v), ((cu_tokens, torch.int32), (start, torch.int32), (block_table, torch.int32),
-                               (cache, torch.uint8), (status, torch.int32)))
-            or k.shape != v.shape or cu_tokens.numel() != n + 1 or block_table.dim() != 2 or block_table.shape[0] != n):
-        return REDLITE_EINVAL
-    T, H, D = k.shape
-    pages = _kv4_pages(cache, H, D, page_size)
-    if pages < 0:
-        return REDLITE_EUNSUPPORTED if redlite_kv4_page_bytes(H, D, page_size) == 0 else REDLITE_EINVAL
-    with torch.cuda.device(k.device):
-        return lib().redlite_kv4_load(_DTYPES[k.dtype], _ptr(cache), H, D, page_size, _ptr(block_table),
-                                      block_table.shape[1], pages, _ptr(cu_tokens), _ptr(start), n, T, _ptr(k), _ptr(v),
-                                      _row_stride(k), _row_stride(v), _ptr(status), _on(k.device, stream))
+    return (_marshal_mod or _marshal()).kv4_load(k, v, cu_tokens, start, block_table, cache, page_size, status,
+                                                 _handle(stream))
 
 
 def redlite_kv4_decode_workspace_bytes(n_seqs: int, n_heads: int, n_kv_heads: int, head_dim: int) -> int:
@@ -405,41 +361,13 @@ def redlite_kv4_decode(q: torch.Tensor, cache: torch.Tensor, page_size: int, blo
                        status: Optional[torch.Tensor] = None, stream=None, n_kv_heads: Optional[int] = None) -> int:
     """One query per sequence, q [n_seqs, n_heads, head_dim], over its first lens[s] cached tokens.
     The cache is a [n_pages, n_kv_heads, ...] tensor, or flat with n_kv_heads given."""
-    if (not _mixer_ok((q, out), ((cache, torch.uint8), (block_table, torch.int32), (lens, torch.int32),
-                                 (status, torch.int32)))
-            or q.shape != out.shape or lens.numel() != q.shape[0] or block_table.dim() != 2
-            or block_table.shape[0] != q.shape[0] or not _dense(workspace, workspace.dtype, q.device)):
-        return REDLITE_EINVAL
-    B, Hq, D = q.shape
-    if n_kv_heads is None:
-        if cache.dim() < 2:
-            return REDLITE_EINVAL
-        n_kv_heads = cache.shape[1]
-    pages = _kv4_pages(cache, n_kv_heads, D, page_size)
-    if pages < 0:
-        return REDLITE_EUNSUPPORTED if redlite_kv4_page_bytes(n_kv_heads, D, page_size) == 0 else REDLITE_EINVAL
-    with torch.cuda.device(q.device):
-        return lib().redlite_kv4_decode(_DTYPES[q.dtype], _ptr(q), _row_stride(q), B, Hq, n_kv_heads, D, _ptr(cache),
-                                        page_size, _ptr(block_table), block_table.shape[1], pages, _ptr(lens),
-                                        float(scale), _ptr(out), _row_stride(out), _ptr(workspace),
-                                        workspace.numel() * workspace.element_size(), _ptr(status),
-                                        _on(q.device, stream))
+    return (_marshal_mod or _marshal()).kv4_decode(q, cache, page_size, block_table, lens, out, workspace, scale,
+                                                   status, _handle(stream), n_kv_heads)
 
 
 def redlite_delta_workspace_bytes(n_tokens: int, n_seqs: int, n_k_heads: int, n_v_heads: int, dk: int,
                                   dv: int) -> int:
     return int(lib().redlite_delta_workspace_bytes(n_tokens, n_seqs, n_k_heads, n_v_heads, dk, dv))
-
-
-def _delta_ok(q, k, v, g, beta, state_in, state_out, slots, out, status, n_seqs) -> bool:
-    f = torch.float32
-    if not _mixer_ok((q, k, v, out), ((g, f), (beta, f), (state_in, f), (state_out, f), (slots, torch.int32),
-                                      (status, torch.int32))):
-        return False
-    rows, hv, dv = v.shape
-    return (q.shape == k.shape and q.shape[0] == rows and out.shape == v.shape and g.shape == (rows, hv)
-            and beta.shape == (rows, hv) and state_out.dim() == 4 and state_out.shape[1:] == (hv, q.shape[2], dv)
-            and (state_in is None or state_in.shape == state_out.shape) and (slots is None or slots.numel() == n_seqs))
 
 
 def redlite_delta_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor,
@@ -448,17 +376,8 @@ def redlite_delta_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: 
                           qk_eps: float = -1.0, status: Optional[torch.Tensor] = None, stream=None) -> int:
     """The gated delta rule over packed sequences: q, k [rows, n_k_heads, dk]; v, out [rows, n_v_heads, dv];
     g, beta [rows, n_v_heads]; states [n_slots, n_v_heads, dk, dv]."""
-    n = cu.numel() - 1
-    if (n < 0 or not _delta_ok(q, k, v, g, beta, state_in, state_out, slots, out, status, n)
-            or not _dense(cu, torch.int32, q.device) or not _dense(workspace, workspace.dtype, q.device)):
-        return REDLITE_EINVAL
-    with torch.cuda.device(q.device):
-        return lib().redlite_delta_prefill(
-            _DTYPES[q.dtype], _ptr(q), _row_stride(q), _ptr(k), _row_stride(k), _ptr(v), _row_stride(v), _ptr(g),
-            _ptr(beta), _ptr(cu), n, q.shape[0], q.shape[1], v.shape[1], q.shape[2], v.shape[2], float(scale),
-            float(qk_eps), _ptr(state_in), _ptr(state_out), _ptr(slots), state_out.shape[0], _ptr(out),
-            _row_stride(out), _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(status),
-            _on(q.device, stream))
+    return (_marshal_mod or _marshal()).delta_prefill(q, k, v, g, beta, cu, state_in, state_out, slots, out, workspace,
+                                                      scale, qk_eps, status, _handle(stream))
 
 
 def redlite_delta_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor,
@@ -466,15 +385,8 @@ def redlite_delta_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: tor
                        out: torch.Tensor, scale: float, qk_eps: float = -1.0, status: Optional[torch.Tensor] = None,
                        stream=None) -> int:
     """One token per sequence (row s is sequence s); arguments as redlite_delta_prefill."""
-    n = q.shape[0]
-    if not _delta_ok(q, k, v, g, beta, state_in, state_out, slots, out, status, n):
-        return REDLITE_EINVAL
-    with torch.cuda.device(q.device):
-        return lib().redlite_delta_step(
-            _DTYPES[q.dtype], _ptr(q), _row_stride(q), _ptr(k), _row_stride(k), _ptr(v), _row_stride(v), _ptr(g),
-            _ptr(beta), n, q.shape[1], v.shape[1], q.shape[2], v.shape[2], float(scale), float(qk_eps), _ptr(state_in),
-            _ptr(state_out), _ptr(slots), state_out.shape[0], _ptr(out), _row_stride(out), _ptr(status),
-            _on(q.device, stream))
+    return (_marshal_mod or _marshal()).delta_step(q, k, v, g, beta, state_in, state_out, slots, out, scale, qk_eps,
+                                                   status, _handle(stream))
 
 
 class SlotPool:

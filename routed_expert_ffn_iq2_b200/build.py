@@ -1,4 +1,5 @@
-"""Build libredlite_moe.so in-tree with nvcc for sm_100a."""
+"""Build libredlite_moe.so in-tree with nvcc for sm_100a, and beside it the
+Python marshaller of the token mixers (_marshal.so, host C++)."""
 
 from __future__ import annotations
 
@@ -6,13 +7,16 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OBJ = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libredlite_moe.so")
+MARSHAL = os.path.join(PKG, "_marshal.so")
 
+CXX = os.environ.get("CXX", "g++")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -29,15 +33,41 @@ def _deps():
     return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + [os.path.join(ROOT, "include", "redlite_moe.h")]
 
 
+def _newer(target: str, deps) -> bool:
+    return os.path.exists(target) and all(os.path.getmtime(p) <= os.path.getmtime(target) for p in deps)
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
-        return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(p) <= t for p in _deps())
+    return _newer(LIB, _deps())
+
+
+def build_marshal(force: bool = False) -> str:
+    """_marshal.so against torch's headers and libredlite_moe.so (found beside it)."""
+    src = os.path.join(CSRC, "marshal.cpp")
+    if not force and _newer(MARSHAL, [src, os.path.join(ROOT, "include", "redlite_moe.h")]):
+        return MARSHAL
+    import torch
+
+    t = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(NVCC))
+    inc = [os.path.join(ROOT, "include"), os.path.join(t, "include"),
+           os.path.join(t, "include", "torch", "csrc", "api", "include"), os.path.join(cuda, "include"),
+           sysconfig.get_paths()["include"]]
+    tmp = MARSHAL + ".tmp"
+    r = subprocess.run([CXX, "-O2", "-std=c++17", "-fPIC", "-shared", *[a for i in inc for a in ("-isystem", i)],
+                        f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", src, "-o", tmp,
+                        "-L", PKG, "-l:libredlite_moe.so", "-Wl,-rpath,$ORIGIN", "-L", os.path.join(t, "lib"),
+                        "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"],
+                       stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+    if r.returncode != 0:
+        raise RuntimeError("marshal.cpp failed:\n" + r.stdout.decode(errors="replace"))
+    os.replace(tmp, MARSHAL)
+    return MARSHAL
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
     if not force and up_to_date():
+        build_marshal()
         return LIB
     os.makedirs(OBJ, exist_ok=True)
     procs, objs = [], []
@@ -61,6 +91,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     subprocess.check_call([NVCC, "-gencode", "arch=compute_100a,code=sm_100a", "-shared", "--cudart", "static",
                            "-o", tmp, *objs])
     os.replace(tmp, LIB)
+    build_marshal(force)
     return LIB
 
 
