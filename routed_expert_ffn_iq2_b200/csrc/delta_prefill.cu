@@ -9,25 +9,30 @@
 //   O = scale (exp(c) Q S0 + P D),  P_ij = exp(c_i - c_j) (Q K^T)_ij (j <= i)
 //   S = exp(c_last) S0 + sum_i exp(c_last - c_i) k_i d_i^T
 // T and P need no state, so delta_prep_kernel forms them for all chunks at
-// once; delta_chain_kernel then walks the chunks of a sequence.  Everything
-// in the chain is linear in the value columns, so a warp takes 16 of them:
-// it keeps S^T [16 x dk] in fp32 accumulators and chains
-//   S^T K^T -> D^T -> S^T, O^T
-// where each product's result is, register for register, the next one's A
-// operand (m16n8k16, M = value columns).  Warps exchange nothing; K, Q, T, P
-// and the per-token factors come through shared memory by bulk copies.  The
-// chain of one head is serial, so the warps per block follow the number of
-// chains: few chains go out as two-warp blocks over all multiprocessors.
+// once; delta_chain_kernel then walks the chunks of a sequence.  Everything in
+// the chain is linear in the value columns, so a warp takes eight of them (the
+// N of m16n8k16) and keeps its S [dk x 8] in fp32 accumulators:
+//   K S -> D -> S
+// each result going through movmatrix into the next product's B operand;
+// columns meet nowhere.  A chain is serial, so the latency of a chunk bounds a
+// call of few sequences: a second warp beside each takes the operands over
+// shared memory and forms Q S + P D, which nothing waits for.  K, Q, T, P and
+// the per-token factors come through shared memory by bulk copies.
 //
-// Precision: bf16 keys and queries enter the products unrounded; everything
-// fp32 that meets a product (the state, T, P, the updates; fp32 and fp16
-// keys and queries) is split in two bf16 parts, hi hi + hi lo + lo hi, which
-// leaves out 2^-17 of each term.  Norms (q, k over their length) and decays
-// multiply results per token in fp32, never the bf16 operands.  Sums of log
-// decays are fp64 and only their differences are rounded.
+// Precision: every operand of a product is held to 2^-22 or better, so the
+// result is that of fp32 arithmetic.  A row is scaled by a power of two that
+// takes its largest element to 2^14 and split in two fp16 parts (11 bits
+// each); products are hi hi + hi lo + lo hi, hi hi + lo hi where the other
+// side (16-bit keys and queries) is one exact part.  bf16 outputs alone are
+// made from the hi parts (2^-12 of each operand, under their own rounding of
+// 2^-8).  Scales, norms (q, k over their length) and decays multiply results
+// per token in fp32.  Sums of log decays are fp64, held as two fp32 numbers
+// whose differences are rounded once.
 //
 // A chunk that meets a NaN or an infinity is walked token by token, so that
 // what lies behind a token never reaches it.
+#include <type_traits>
+
 #include "delta.cuh"
 
 namespace redlite {
@@ -35,13 +40,15 @@ namespace {
 
 constexpr int C = 64;  // tokens of a chunk
 
-// Per (chunk, value head): T and P as two bf16 planes each, the ten 16 x 16
-// blocks on and under the diagonal (row by row of blocks), a block's rows 32
-// bytes, their two 16-byte pieces swapped in every other group of four rows
-// (no bank conflicts); then eight per-token factors.
+// Per (chunk, value head): T and P as two fp16 planes each (rows scaled), the
+// ten 16 x 16 blocks on and under the diagonal (row by row of blocks), a
+// block's rows 32 bytes, their two 16-byte pieces swapped in every other group
+// of four rows (no bank conflicts); then ten per-token factors.
 constexpr int kPlane = 10 * 512;
 enum { kThi, kTlo, kPhi, kPlo, kPlanes };
-enum { fBeta, fR, fQ, fK, fAlpha, fNk, fNq, fLast, kFactors };  // fLast: [0] = exp(c_last)
+// fLast: [0] = exp(c_last); fT, fP: inverse scales of the rows of T and P;
+// fR, fQ, fK, fNk, fNq hold the inverse scales of the keys' and queries' rows
+enum { fBeta, fR, fQ, fK, fAlpha, fNk, fNq, fLast, fT, fP, kFactors };
 constexpr int kHeadBlock = kPlanes * kPlane + kFactors * C * 4;
 
 // Per (chunk, key head): K and Q tiles (NK planes each), rows of 2 DK bytes,
@@ -73,50 +80,134 @@ __device__ __forceinline__ Span seq_span(const DeltaArgs &a, int s) {
 }
 
 struct WsPlan {
-  size_t kq, head, total;
+  size_t kq, head, order, total;
 };
-inline WsPlan ws_plan(int64_t slots, int n_k, int n_v, int dk) {
+inline WsPlan ws_plan(int64_t slots, int n_seqs, int n_k, int n_v, int dk) {
   WsPlan w;
   w.kq = 0;
   w.head = align256((size_t)slots * n_k * (2 * 2 * C * (size_t)dk * 2));
-  w.total = align256(w.head + (size_t)slots * n_v * kHeadBlock);
+  w.order = align256(w.head + (size_t)slots * n_v * kHeadBlock);
+  w.total = align256(w.order + (size_t)n_seqs * 4);
   return w;
 }
 
 // ------------------------------------------------------------------- prep
 
-// Row i of T = (I + A)^-1 in registers, from T (I + A) = I:
-//   t_j = (i == j) - sum_{k > j} t_k A_kj,  j = N - 1 .. 0
-// A^T is read as broadcasts; rows above N are zero for this warp.
-template <int N>
-__device__ __forceinline__ void solve_row(const float *at, int i, float (&t)[C]) {
-#pragma unroll
-  for (int j = N - 1; j >= 0; --j) {
-    float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
-#pragma unroll
-    for (int k4 = j / 4; k4 < N / 4; ++k4) {
-      const float4 x = *reinterpret_cast<const float4 *>(at + j * 68 + 4 * k4);
-      if (4 * k4 > j) s0 = fmaf(t[4 * k4], x.x, s0);
-      if (4 * k4 + 1 > j) s1 = fmaf(t[4 * k4 + 1], x.y, s1);
-      if (4 * k4 + 2 > j) s2 = fmaf(t[4 * k4 + 2], x.z, s2);
-      if (4 * k4 + 3 > j) s3 = fmaf(t[4 * k4 + 3], x.w, s3);
+// The sequences by falling length (in steps of half a power of two), so that
+// the chains that take longest start first.  One block.
+__device__ void order_sequences(const DeltaArgs &a, int32_t *order, int *bucket) {
+  const auto key = [&](int s) {
+    const Span sp = seq_span(a, s);
+    const unsigned n = (unsigned)((max(sp.len, 0) + C - 1) / C);
+    if (n < 2) return 63 - (int)n;
+    const int b = 31 - __clz(n);
+    return 63 - (2 * b + (int)((n >> (b - 1)) & 1));
+  };
+  for (int i = threadIdx.x; i < 64; i += blockDim.x) bucket[i] = 0;
+  __syncthreads();
+  for (int s = threadIdx.x; s < a.n_seqs; s += blockDim.x) atomicAdd(bucket + key(s), 1);
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    int sum = 0;
+    for (int i = 0; i < 64; ++i) {
+      const int n = bucket[i];
+      bucket[i] = sum, sum += n;
     }
-    t[j] = (i == j ? 1.f : 0.f) - ((s0 + s1) + (s2 + s3));
+  }
+  __syncthreads();
+  for (int s = threadIdx.x; s < a.n_seqs; s += blockDim.x) order[atomicAdd(bucket + key(s), 1)] = s;
+}
+
+constexpr int kPitchA = 68;                  // fp32 rows of A: B operands are read without bank conflicts
+constexpr int kHeadA = C * kPitchA + 16;     // A of one head
+constexpr int kPitchT = 20;                  // rows of a diagonal block of T
+template <int NK, int DK>
+__host__ __device__ constexpr int prep_smem() {
+  return kq_bytes<NK, DK>() > 2 * kHeadA * 4 ? kq_bytes<NK, DK>() : 2 * kHeadA * 4;
+}
+
+// Y[16x16] += X[16x16] B[16x16] in tf32 parts (hi hi + hi lo + lo hi).  X: two
+// accumulator tiles of 8 columns; B: fp32 rows of `pitch` in shared memory.
+// The sum runs over the columns in the order in which X holds them.
+__device__ __forceinline__ void block_product(float (&Y)[2][4], const float (&X)[2][4], const float *B, int pitch,
+                                              int lane) {
+  const int r = lane >> 2, c = lane & 3;
+#pragma unroll
+  for (int kb = 0; kb < 2; ++kb) {
+    uint32_t h[4], l[4];
+    split_tf32(X[kb][0], h[0], l[0]), split_tf32(X[kb][2], h[1], l[1]);
+    split_tf32(X[kb][1], h[2], l[2]), split_tf32(X[kb][3], h[3], l[3]);
+#pragma unroll
+    for (int nb = 0; nb < 2; ++nb) {
+      const float *p = B + (8 * kb + 2 * c) * pitch + 8 * nb + r;
+      uint32_t b0, d0, b1, d1;
+      split_tf32(p[0], b0, d0), split_tf32(p[pitch], b1, d1);
+      mma_tf32(Y[nb], h, b0, b1);
+      mma_tf32(Y[nb], l, b0, b1);
+      mma_tf32(Y[nb], h, d0, d1);
+    }
   }
 }
 
-// One block per (chunk slot, key head), four warps: warp w takes rows 16 w ..
-// of the two Gram matrices; then the value heads of the key head go in pairs,
-// two warps (64 rows of T) each.
+// Rows r and r + 8 of a 16-row block (NB tiles of 8 columns, zeros from the
+// n-th on; the t-th is that of columns 8 tile(t) ..): the scaled fp16 parts to
+// two planes, the inverse scales to f.
+struct SameTile {
+  __device__ __forceinline__ int operator()(int t) const { return t; }
+};
+template <int NB, typename Get, typename Tile = SameTile>
+__device__ __forceinline__ void store_rows(uint8_t *hi, uint8_t *lo, float *f, int block, int n, int lane, Get get,
+                                           Tile tile = Tile()) {
+  const int r = lane >> 2, c = lane & 3;
+  float m0 = 0.f, m1 = 0.f;
+#pragma unroll
+  for (int t = 0; t < NB; ++t) {
+    const float *v = get(t);
+    m0 = fmaxf(m0, fmaxf(fabsf(v[0]), fabsf(v[1]))), m1 = fmaxf(m1, fmaxf(fabsf(v[2]), fabsf(v[3])));
+  }
+#pragma unroll
+  for (int o = 1; o <= 2; o <<= 1) {
+    m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, o));
+    m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, o));
+  }
+  float i0, i1;
+  const float s0 = scale_f16(m0, i0), s1 = scale_f16(m1, i1);
+  if (c == 0) f[16 * block + r] = i0, f[16 * block + r + 8] = i1;
+#pragma unroll
+  for (int t = 0; t < NB; ++t) {
+    if (t >= n) break;
+    const float *v = get(t);
+    uint32_t h0, l0, h1, l1;
+    split_f16(v[0] * s0, v[1] * s0, h0, l0);
+    split_f16(v[2] * s1, v[3] * s1, h1, l1);
+    const uint32_t o0 = tp_off(16 * block + r, tile(t)) + 4 * c, o1 = tp_off(16 * block + r + 8, tile(t)) + 4 * c;
+    *reinterpret_cast<uint32_t *>(hi + o0) = h0, *reinterpret_cast<uint32_t *>(lo + o0) = l0;
+    *reinterpret_cast<uint32_t *>(hi + o1) = h1, *reinterpret_cast<uint32_t *>(lo + o1) = l1;
+  }
+}
+
+// One block per (chunk slot, key head), eight warps.  The first four make
+// K K^T and from it A (rows 16 role ..) and the diagonal blocks of T, the
+// others Q K^T and P; roles turn with the block, since role 3 has most of the
+// work and a warp's scheduler goes by its number.  The value heads of the key
+// head go in pairs.  T is found by blocks of 16: the diagonal ones by
+// substitution, a row per lane, then, in each row of blocks from the diagonal
+// outwards,
+//   T_wj = -(sum_{j < k <= w} T_wk A_kj) T_jj
+// on the tensor cores, a warp per head and row of blocks.
 template <typename T, int NK, int DK>
-__global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaArgs a, const WsPlan w) {
+__global__ void __launch_bounds__(256, 2) delta_prep_kernel(const DeltaArgs a, const WsPlan w) {
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ double sc[2][C];
-  __shared__ float snk[C], snq[C], sb[2][C], sg[2][C];
+  __shared__ double tail[2];
+  __shared__ float2 sc[2][C];  // sums of log2 decays: high and low part
+  __shared__ float snk[C], snq[C], sb[2][C];
+  __shared__ __align__(16) float td[2][4][16 * kPitchT];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, c = lane & 3;
+  if (blockIdx.x == 0 && blockIdx.y == 0)
+    order_sequences(a, reinterpret_cast<int32_t *>(a.ws + w.order), reinterpret_cast<int *>(smem));
   const int64_t slot = blockIdx.x;
-  const int kh = blockIdx.y;
+  const int kh = blockIdx.y, role = (warp + blockIdx.x) & 3, group = warp >> 2;
   // the last sequence whose first slot is not behind this one
   int lo = 0, hi = a.n_seqs;
   while (hi - lo > 1) {
@@ -129,63 +220,76 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaArgs a, cons
   if (sp.len < 0 || idx < 0 || idx * C >= sp.len) return;
   const int n = min(C, sp.len - (int)idx * C);
   const int64_t row0 = (int64_t)sp.start + idx * C;
+  __syncthreads();
 
-  // ---- K and Q rows: bf16 parts into shared memory and the workspace, sums of squares
-  constexpr int kPieces = DK / 8, kTile = C * DK * 2;
+  // ---- K and Q rows: scaled fp16 parts into shared memory and the workspace,
+  // sums of squares; four pieces of a thread are on their way at a time
+  constexpr int kPieces = DK / 8, kTile = C * DK * 2, kRounds = 2 * C * kPieces / 256, kAhead = 4;
   uint8_t *kq = a.ws + w.kq + ((size_t)slot * a.n_k + kh) * kq_bytes<NK, DK>();
-#pragma unroll 4
-  for (int it = 0; it < 2 * C * kPieces / 128; ++it) {
-    const int id = it * 128 + tid, which = id / (C * kPieces), row = id / kPieces % C, piece = id % kPieces;
-    float x[8];
-    if (row < n) {
-      load8<T>((which ? (const T *)a.q + (row0 + row) * a.q_stride : (const T *)a.k + (row0 + row) * a.k_stride) +
-                   (int64_t)kh * DK + piece * 8,
-               x);
-    } else {
+#pragma unroll 1
+  for (int r0 = 0; r0 < kRounds; r0 += kAhead) {
+    float x[kAhead][8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = 0.f;
-    }
-    float ss = 0.f;
+    for (int it = 0; it < kAhead; ++it) {
+      const int id = (r0 + it) * 256 + tid, which = id / (C * kPieces), row = id / kPieces % C, piece = id % kPieces;
+      if (row < n) {
+        load8<T>((which ? (const T *)a.q + (row0 + row) * a.q_stride : (const T *)a.k + (row0 + row) * a.k_stride) +
+                     (int64_t)kh * DK + piece * 8,
+                 x[it]);
+      } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-#pragma unroll
-    for (int o = 1; o < kPieces; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    if (piece == 0) {
-      const float f = a.qk_eps >= 0.f ? 1.f / sqrtf(ss + a.qk_eps) : 1.f;
-      (which ? snq : snk)[row] = f;
+        for (int e = 0; e < 8; ++e) x[it][e] = 0.f;
+      }
     }
 #pragma unroll
-    for (int p = 0; p < NK; ++p) {
-      uint4 v;
-      v.x = pack_bf16(x[0], x[1]), v.y = pack_bf16(x[2], x[3]);
-      v.z = pack_bf16(x[4], x[5]), v.w = pack_bf16(x[6], x[7]);
-      const uint32_t off = (which * NK + p) * kTile + kq_off<DK>(row, piece);
+    for (int it = 0; it < kAhead; ++it) {
+      const int id = (r0 + it) * 256 + tid, which = id / (C * kPieces), row = id / kPieces % C, piece = id % kPieces;
+      float ss = 0.f, mx = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ss = fmaf(x[it][e], x[it][e], ss), mx = fmaxf(mx, fabsf(x[it][e]));
+#pragma unroll
+      for (int o = 1; o < kPieces; o <<= 1) {
+        ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      }
+      float inv;
+      const float s = scale_f16(mx, inv);
+      if (piece == 0) {
+        const float f = a.qk_eps >= 0.f && row < n ? 1.f / sqrtf(ss + a.qk_eps) : 1.f;
+        (which ? snq : snk)[row] = f * inv;
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[it][e] *= s;
+      uint4 v, u;
+      split_f16(x[it][0], x[it][1], v.x, u.x), split_f16(x[it][2], x[it][3], v.y, u.y);
+      split_f16(x[it][4], x[it][5], v.z, u.z), split_f16(x[it][6], x[it][7], v.w, u.w);
+      const uint32_t off = which * NK * kTile + kq_off<DK>(row, piece);
       *reinterpret_cast<uint4 *>(smem + off) = v;
       *reinterpret_cast<uint4 *>(kq + off) = v;
-      x[0] -= bf16_lo(v.x), x[1] -= bf16_hi(v.x), x[2] -= bf16_lo(v.y), x[3] -= bf16_hi(v.y);
-      x[4] -= bf16_lo(v.z), x[5] -= bf16_hi(v.z), x[6] -= bf16_lo(v.w), x[7] -= bf16_hi(v.w);
+      if (NK == 2) {
+        *reinterpret_cast<uint4 *>(smem + off + kTile) = u;
+        *reinterpret_cast<uint4 *>(kq + off + kTile) = u;
+      }
     }
   }
   __syncthreads();
-  // ---- rows 16 warp .. of K K^T and Q K^T
-  float G[8][4], H[8][4];
+  // ---- rows 16 role .. of K K^T (first group) or Q K^T
+  float G[8][4];
 #pragma unroll
   for (int t = 0; t < 8; ++t)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) G[t][e] = H[t][e] = 0.f;
+    for (int e = 0; e < 4; ++e) G[t][e] = 0.f;
   const uint32_t base = ptx::smem_u32(smem);
 #pragma unroll
   for (int ks = 0; ks < DK / 16; ++ks) {
-    uint32_t ak[NK][4], aq[NK][4];
-    const int arow = 16 * warp + (lane & 15), apiece = 2 * ks + (lane >> 4);
+    uint32_t ar[NK][4];
+    const int arow = 16 * role + (lane & 15), apiece = 2 * ks + (lane >> 4);
 #pragma unroll
-    for (int p = 0; p < NK; ++p) {
-      ldsm4(base + p * kTile + kq_off<DK>(arow, apiece), ak[p][0], ak[p][1], ak[p][2], ak[p][3]);
-      ldsm4(base + (NK + p) * kTile + kq_off<DK>(arow, apiece), aq[p][0], aq[p][1], aq[p][2], aq[p][3]);
-    }
+    for (int p = 0; p < NK; ++p)
+      ldsm4(base + (group * NK + p) * kTile + kq_off<DK>(arow, apiece), ar[p][0], ar[p][1], ar[p][2], ar[p][3]);
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-      if (t > warp) break;  // columns behind the rows are not needed
+      if (t > role) break;  // columns behind the rows are not needed
       const int brow = 16 * t + (lane & 7) + ((lane >> 4) << 3), bpiece = 2 * ks + ((lane >> 3) & 1);
 #pragma unroll
       for (int p = 0; p < NK; ++p) {
@@ -194,148 +298,299 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaArgs a, cons
 #pragma unroll
         for (int s = 0; s + p < NK; ++s)
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            mma_bf16(G[2 * t + u], ak[s][0], ak[s][1], ak[s][2], ak[s][3], b[2 * u], b[2 * u + 1]);
-            mma_bf16(H[2 * t + u], aq[s][0], aq[s][1], aq[s][2], aq[s][3], b[2 * u], b[2 * u + 1]);
-          }
+          for (int u = 0; u < 2; ++u) mma_f16(G[2 * t + u], ar[s], b[2 * u], b[2 * u + 1]);
       }
     }
   }
-  float *at = reinterpret_cast<float *>(smem);  // A^T of two heads, [64][68] each (the tiles are read)
+  float *sa = reinterpret_cast<float *>(smem);  // A of two heads (the tiles are read)
   const int per = a.n_v / a.n_k;
   for (int h0 = 0; h0 < per; h0 += 2) {
     __syncthreads();
-    // ---- factors per token: thread t of a half takes token t of its head
+    // ---- factors per token: of the first four warps, two take a head
     const int half = tid >> 6, tok = tid & 63, head = kh * per + h0 + half;
-    const bool have = h0 + half < per;
+    const bool have = half < 2 && h0 + half < per;
     float g = 0.f, b = 0.f;
     if (have && tok < n) {
       g = delta_clamp_g(__ldg(a.g + (row0 + tok) * a.n_v + head));
       b = __ldg(a.beta + (row0 + tok) * a.n_v + head);
     }
     double sum = g;
+    if (half < 2) {
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const double v = __shfl_up_sync(0xffffffffu, sum, o);
-      if (lane >= o) sum += v;
+      for (int o = 1; o < 32; o <<= 1) {
+        const double v = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += v;
+      }
+      if (tok == 31) tail[half] = sum;
     }
-    sc[half][tok] = sum, sb[half][tok] = b, sg[half][tok] = g;
     __syncthreads();
-    if (tok >= 32) sum += sc[half][31];
+    if (half < 2) {
+      if (tok >= 32) sum += tail[half];
+      const double z = sum * 1.4426950408889634074;
+      const float zh = (float)z;
+      sc[half][tok] = make_float2(zh, (float)(z - (double)zh)), sb[half][tok] = b;
+    }
     __syncthreads();
-    sc[half][tok] = sum;
-    __syncthreads();
+    // 2 to the difference of two sums: what is rounded is the difference
+    auto decay = [&](float2 x, float2 y) { return ex2((x.x - y.x) + (x.y - y.y)); };
     if (have) {
       float *f = reinterpret_cast<float *>(a.ws + w.head + ((size_t)slot * a.n_v + head) * kHeadBlock +
                                            kPlanes * kPlane);
-      const double last = sc[half][C - 1];
-      const float gamma = expf((float)sum);
+      const float2 none = make_float2(0.f, 0.f), mine = sc[half][tok], last = sc[half][C - 1];
+      const float gamma = decay(mine, none);
       f[fBeta * C + tok] = b;
       f[fR * C + tok] = b * gamma * snk[tok];
       f[fQ * C + tok] = tok < n ? a.scale * snq[tok] * gamma : 0.f;
-      f[fK * C + tok] = tok < n ? snk[tok] * expf((float)(last - sum)) : 0.f;
+      f[fK * C + tok] = tok < n ? snk[tok] * decay(last, mine) : 0.f;
       f[fAlpha * C + tok] = expf(g);
       f[fNk * C + tok] = snk[tok];
       f[fNq * C + tok] = a.scale * snq[tok];
-      f[fLast * C + tok] = expf((float)last);
+      f[fLast * C + tok] = decay(last, none);
     }
-    // ---- A^T (shared) and P (workspace) of both heads
-#pragma unroll
+    // ---- A (shared) or P (workspace) of both heads.  In front of the diagonal
+    // block a decay is the product of that from the column to the block's
+    // first row and that from there to the row.
+#pragma unroll 1
     for (int q = 0; q < 2; ++q) {
       if (h0 + q >= per) break;
       uint8_t *blk = a.ws + w.head + ((size_t)slot * a.n_v + kh * per + h0 + q) * kHeadBlock;
-      float *ah = at + q * C * 68;
+      const int i0 = 16 * role + r, i1 = i0 + 8;
+      const float2 c0 = sc[q][i0], c1 = sc[q][i1], cb = sc[q][16 * role];
+      const float w0 = group ? a.scale * snq[i0] : sb[q][i0] * snk[i0];
+      const float w1 = group ? a.scale * snq[i1] : sb[q][i1] * snk[i1];
+      const float e0 = w0 * decay(c0, cb), e1 = w1 * decay(c1, cb);
+      float v[8][4];
 #pragma unroll
       for (int t = 0; t < 8; ++t) {
-        float pv[4];
+        const int j = 8 * t + 2 * c;
+        if ((t >> 1) < role) {
+          const float f0 = decay(cb, sc[q][j]) * snk[j], f1 = decay(cb, sc[q][j + 1]) * snk[j + 1];
+          v[t][0] = e0 * f0 * G[t][0], v[t][1] = e0 * f1 * G[t][1];
+          v[t][2] = e1 * f0 * G[t][2], v[t][3] = e1 * f1 * G[t][3];
+        } else if ((t >> 1) == role) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int i = 16 * warp + r + 8 * (e >> 1), j = 8 * t + 2 * c + (e & 1);
-          float x = 0.f, y = 0.f;
-          if (j <= i) {
-            const float dec = expf((float)(sc[q][i] - sc[q][j])) * snk[j];
-            y = a.scale * snq[i] * dec * H[t][e];
-            if (j < i) x = sb[q][i] * snk[i] * dec * G[t][e];
+          for (int e = 0; e < 4; ++e) {
+            const int i = e < 2 ? i0 : i1, jj = j + (e & 1);
+            v[t][e] = jj < i || (jj == i && group) ? (e < 2 ? w0 : w1) * decay(e < 2 ? c0 : c1, sc[q][jj]) * snk[jj] * G[t][e]
+                                                   : 0.f;
           }
-          ah[j * 68 + i] = x;
-          pv[e] = y;
+        } else {
+          v[t][0] = v[t][1] = v[t][2] = v[t][3] = 0.f;
         }
-        if ((t >> 1) <= warp) {
+      }
+      if (group) {
+        store_rows<8>(blk + kPhi * kPlane, blk + kPlo * kPlane,
+                      reinterpret_cast<float *>(blk + kPlanes * kPlane) + fP * C, role, 2 * role + 2, lane,
+                      [&](int t) { return v[t]; });
+      } else {
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            uint32_t ph, pl;
-            split_bf16(pv[2 * e], pv[2 * e + 1], ph, pl);
-            const uint32_t off = tp_off(16 * warp + r + 8 * e, t) + 4 * c;
-            *reinterpret_cast<uint32_t *>(blk + kPhi * kPlane + off) = ph;
-            *reinterpret_cast<uint32_t *>(blk + kPlo * kPlane + off) = pl;
+        for (int t = 0; t < 8; ++t) {
+          if ((t >> 1) > role) break;
+          float *p = sa + q * kHeadA + i0 * kPitchA + 8 * t + 2 * c;
+          *reinterpret_cast<float2 *>(p) = make_float2(v[t][0], v[t][1]);
+          *reinterpret_cast<float2 *>(p + 8 * kPitchA) = make_float2(v[t][2], v[t][3]);
+        }
+      }
+    }
+    // ---- diagonal blocks of T: lane 16 q + i has row i of head q's block
+    if (!group) {
+      __syncwarp();
+      const int q = lane >> 4, i = lane & 15;
+      const float *ad = sa + q * kHeadA + 16 * role * kPitchA + 16 * role;
+      float t[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) t[j] = i == j ? 1.f : 0.f;
+      if (h0 + q < per) {
+#pragma unroll
+        for (int k = 15; k > 0; --k) {
+#pragma unroll
+          for (int j4 = 0; j4 < (k + 3) / 4; ++j4) {
+            const float4 x = *reinterpret_cast<const float4 *>(ad + k * kPitchA + 4 * j4);
+            const float y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (4 * j4 + e < k) t[4 * j4 + e] = fmaf(-t[k], y[e], t[4 * j4 + e]);
           }
         }
       }
+#pragma unroll
+      for (int j = 0; j < 16; j += 4)
+        *reinterpret_cast<float4 *>(&td[q][role][i * kPitchT + j]) = make_float4(t[j], t[j + 1], t[j + 2], t[j + 3]);
     }
     __syncthreads();
-    // ---- T, a row per thread
-    if (have) {
-      float t[C];
-      const int i = tok;
-      if (tok < 32) {
+    // ---- the rest of row block `role` of head q: tiles by their distance d from the diagonal
+    const int q = group;
+    if (h0 + q >= per) continue;
+    uint8_t *blk = a.ws + w.head + ((size_t)slot * a.n_v + kh * per + h0 + q) * kHeadBlock;
+    float X[4][2][4];
 #pragma unroll
-        for (int j = 32; j < C; ++j) t[j] = 0.f;
-        solve_row<32>(at + half * C * 68, i, t);
-      } else {
-        solve_row<64>(at + half * C * 68, i, t);
-      }
-      uint8_t *blk = a.ws + w.head + ((size_t)slot * a.n_v + head) * kHeadBlock;
+    for (int d = 0; d < 4; ++d)
 #pragma unroll
-      for (int p = 0; p < 8; ++p) {
-        if ((p >> 1) > (i >> 4)) break;
-        uint4 vh, vl;
-        split_bf16(t[8 * p], t[8 * p + 1], vh.x, vl.x);
-        split_bf16(t[8 * p + 2], t[8 * p + 3], vh.y, vl.y);
-        split_bf16(t[8 * p + 4], t[8 * p + 5], vh.z, vl.z);
-        split_bf16(t[8 * p + 6], t[8 * p + 7], vh.w, vl.w);
-        *reinterpret_cast<uint4 *>(blk + kThi * kPlane + tp_off(i, p)) = vh;
-        *reinterpret_cast<uint4 *>(blk + kTlo * kPlane + tp_off(i, p)) = vl;
-      }
+      for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) X[d][nb][e] = 0.f;
+#pragma unroll
+    for (int nb = 0; nb < 2; ++nb) {
+      const float *p = &td[q][role][r * kPitchT + 8 * nb + 2 * c];
+      X[0][nb][0] = p[0], X[0][nb][1] = p[1], X[0][nb][2] = p[8 * kPitchT], X[0][nb][3] = p[8 * kPitchT + 1];
     }
+#pragma unroll
+    for (int d = 1; d < 4; ++d) {
+      if (d > role) break;
+      const int j = role - d;
+      float Y[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+      for (int e = 0; e < d; ++e)
+        block_product(Y, X[e], sa + q * kHeadA + 16 * (role - e) * kPitchA + 16 * j, kPitchA, lane);
+#pragma unroll
+      for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) Y[nb][e] = -Y[nb][e];
+      block_product(X[d], Y, td[q][j], kPitchT, lane);
+    }
+    // columns 16 (role - d) + 8 nb of the row: tile 2 (role - d) + nb
+    store_rows<8>(blk + kThi * kPlane, blk + kTlo * kPlane, reinterpret_cast<float *>(blk + kPlanes * kPlane) + fT * C,
+                  role, 2 * role + 2, lane, [&](int t) { return X[t >> 1][t & 1]; }, [&](int t) {
+                    return 2 * (role - (t >> 1)) + (t & 1);
+                  });
   }
 }
 
 // ------------------------------------------------------------------ chain
 
-template <typename T>
-struct VTile {
-  static constexpr int kPitch = sizeof(T) == 4 ? 20 : 24;  // elements per token row of 16 (no bank conflicts)
-  static constexpr int kBytes = C * kPitch * (int)sizeof(T);
+constexpr int kChains = 4;            // chain warps per block, and as many output warps
+constexpr int kCols = 8 * kChains;    // value columns per block
+
+// What a chain warp hands to the output warp beside it, per chunk.
+template <bool LO>
+struct Handoff {
+  uint4 s[LO ? 2 : 1][4][32];  // S as B operands, 32 keys each: hi parts, lo parts
+  float4 d[4][32];             // D, 16 tokens each
+  float2 scale[4];             // of S's columns 2 c, 2 c + 1
+  int walk;                    // the chain warp writes this chunk's outputs
+};
+template <int kStages>
+struct ChainBars {
+  uint64_t full[kStages], empty[kStages];
+  uint64_t s_ready[kChains], s_taken[kChains], d_ready[kChains], d_taken[kChains];
+};
+// The plan of a chain block's shared memory.
+template <typename T, int NK, int DK>
+struct Chain {
+  static constexpr bool kLo = !std::is_same<T, __nv_bfloat16>::value;  // outputs from both parts
+  static constexpr int kStage = kq_bytes<NK, DK>() + kHeadBlock;
+  static constexpr int kV = C * 8 * (int)sizeof(T);  // a chain warp's values of a chunk
+  static constexpr int kRest = 2 * kChains * kV + kChains * (int)sizeof(Handoff<kLo>) + (int)sizeof(ChainBars<3>);
+  static constexpr int kStages = 3 * kStage + kRest <= 227 * 1024 ? 3 : 2;
+  static constexpr int kSmem = kStages * kStage + kRest;
+  static_assert(kSmem <= 227 * 1024, "shared memory of a chain block");
 };
 
-template <int NK, int DK>
-__host__ __device__ constexpr int stage_bytes() {
-  return kq_bytes<NK, DK>() + kHeadBlock;
+// Largest of columns 2 c and 2 c + 1 over the rows of a warp's tiles.
+__device__ __forceinline__ void col_max(float &m0, float &m1) {
+#pragma unroll
+  for (int o = 4; o <= 16; o <<= 1) {
+    m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, o));
+    m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, o));
+  }
 }
-constexpr int kStages = 2;
-template <typename T, int NK, int DK, int W>
-__host__ __device__ constexpr int chain_smem() {
-  return kStages * stage_bytes<NK, DK>() + 2 * W * VTile<T>::kBytes + 64;
+// The B operand of 16 rows from an accumulator tile, columns scaled, in two parts.
+__device__ __forceinline__ void split_tile(const float (&x)[4], float s0, float s1, uint32_t (&h)[2], uint32_t (&l)[2]) {
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    split_f16(x[2 * e] * s0, x[2 * e + 1] * s1, h[e], l[e]);
+    h[e] = movm(h[e]), l[e] = movm(l[e]);
+  }
 }
+__device__ __forceinline__ void zero(float (&x)[4][4]) {
+#pragma unroll
+  for (int t = 0; t < 4; ++t) x[t][0] = x[t][1] = x[t][2] = x[t][3] = 0.f;
+}
+// acc (+)= tiles [64 x 16] (rows in shared memory) times a B operand of 16 rows.
+template <int DK>
+__device__ __forceinline__ void load_rows(uint32_t tile, int ks, int lane, uint32_t (&a)[4][4]) {
+#pragma unroll
+  for (int t = 0; t < 4; ++t)
+    ldsm4(tile + kq_off<DK>(16 * t + (lane & 15), 2 * ks + (lane >> 4)), a[t][0], a[t][1], a[t][2], a[t][3]);
+}
+// acc = L B: the lower triangle's blocks (two planes) times the B operands of 64 rows.
+template <bool LO>
+__device__ __forceinline__ void triangle(float (&acc)[4][4], uint32_t planes, const uint32_t (&h)[4][2],
+                                         const uint32_t (&l)[4][2], int lane) {
+  float more[4][4];
+  zero(acc), zero(more);
+#pragma unroll
+  for (int ks = 0; ks < 4; ++ks) {
+    uint32_t p[4][4], q[4][4];
+#pragma unroll
+    for (int t = ks; t < 4; ++t) {
+      const uint32_t off = planes + tp_off(16 * t + (lane & 15), 2 * ks + (lane >> 4));
+      ldsm4(off, p[t][0], p[t][1], p[t][2], p[t][3]);
+      if (LO) ldsm4(off + kPlane, q[t][0], q[t][1], q[t][2], q[t][3]);
+    }
+#pragma unroll
+    for (int t = ks; t < 4; ++t) mma_f16(acc[t], p[t], h[ks][0], h[ks][1]);
+    if (LO) {
+#pragma unroll
+      for (int t = ks; t < 4; ++t) mma_f16(more[t], p[t], l[ks][0], l[ks][1]);
+#pragma unroll
+      for (int t = ks; t < 4; ++t) mma_f16(more[t], q[t], h[ks][0], h[ks][1]);
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < 4; ++t)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[t][e] += more[t][e];
+}
+template <typename T>
+__device__ __forceinline__ void store2(T *p, float x, float y);
+template <>
+__device__ __forceinline__ void store2<float>(float *p, float x, float y) {
+  *reinterpret_cast<float2 *>(p) = make_float2(x, y);
+}
+template <>
+__device__ __forceinline__ void store2<__nv_bfloat16>(__nv_bfloat16 *p, float x, float y) {
+  *reinterpret_cast<uint32_t *>(p) = pack_bf16(x, y);
+}
+template <>
+__device__ __forceinline__ void store2<__half>(__half *p, float x, float y) {
+  *reinterpret_cast<uint32_t *>(p) = pack_f16(x, y);
+}
+__device__ __forceinline__ float2 load2(const float *p) { return *reinterpret_cast<const float2 *>(p); }
+__device__ __forceinline__ float2 load2(const __nv_bfloat16 *p) {
+  return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(p));
+}
+__device__ __forceinline__ float2 load2(const __half *p) { return __half22float2(*reinterpret_cast<const __half2 *>(p)); }
 
-// W chain warps and one that issues the copies.  Block: (slice of 16 W value
-// columns, value head, sequence).
-template <typename T, int NK, int DK, int W>
-__global__ void __launch_bounds__(32 * (W + 1), 1) delta_chain_kernel(const DeltaArgs a, const WsPlan w) {
+// Four chain warps, four output warps and one warp that issues the copies.
+// Block: (slice of 32 value columns, value head, sequence by falling length).
+template <typename T, int NK, int DK>
+__global__ void __launch_bounds__(32 * (2 * kChains + 1), 1) delta_chain_kernel(const DeltaArgs a, const WsPlan w,
+                                                                                  const bool ordered) {
   extern __shared__ __align__(128) uint8_t smem[];
-  constexpr int kStage = stage_bytes<NK, DK>(), kTile = C * DK * 2, NT = DK / 8;
+  using Plan = Chain<T, NK, DK>;
+  constexpr int kStages = Plan::kStages, kStage = Plan::kStage, kTile = C * DK * 2, NT = DK / 16;
+  constexpr bool kLo = Plan::kLo;
   uint8_t *vbuf = smem + kStages * kStage;
-  uint64_t *full = reinterpret_cast<uint64_t *>(vbuf + 2 * W * VTile<T>::kBytes), *empty = full + kStages;
+  Handoff<kLo> *handoff = reinterpret_cast<Handoff<kLo> *>(vbuf + 2 * kChains * Plan::kV);
+  ChainBars<kStages> *bars = reinterpret_cast<ChainBars<kStages> *>(handoff + kChains);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, c = lane & 3;
-  const int slices = a.dv / (16 * W);
-  const int slice = blockIdx.x % slices, head = blockIdx.x / slices % a.n_v, seq = blockIdx.x / (slices * a.n_v);
+  const int slices = a.dv / kCols;
+  const int slice = blockIdx.x % slices, head = blockIdx.x / slices % a.n_v;
   const int kh = head / (a.n_v / a.n_k);
-  if (tid == 0)
-    for (int i = 0; i < kStages; ++i) ptx::mbar_init(full + i, 1), ptx::mbar_init(empty + i, W);
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) ptx::mbar_init(bars->full + i, 1), ptx::mbar_init(bars->empty + i, 2 * kChains);
+    for (int i = 0; i < kChains; ++i) {
+      ptx::mbar_init(bars->s_ready + i, 1), ptx::mbar_init(bars->s_taken + i, 1);
+      ptx::mbar_init(bars->d_ready + i, 1), ptx::mbar_init(bars->d_taken + i, 1);
+    }
+  }
   ptx::mbar_fence_init();
   // in front of every way out: this grid must not end before the one that
   // writes the workspace
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  int seq = blockIdx.x / (slices * a.n_v);
+  if (ordered) seq = *reinterpret_cast<const int32_t *>(a.ws + w.order + 4 * (size_t)seq);
   const int64_t slot = delta_slot(a, seq);
   __syncthreads();
   const Span sp = seq_span(a, seq);
@@ -345,56 +600,137 @@ __global__ void __launch_bounds__(32 * (W + 1), 1) delta_chain_kernel(const Delt
   }
   const int n_chunks = (sp.len + C - 1) / C;
   if (slot < 0) {
-    for (int i = tid; i < sp.len * 16 * W; i += blockDim.x)
-      ((T *)a.out)[(int64_t)(sp.start + i / (16 * W)) * a.out_stride + (int64_t)head * a.dv + slice * 16 * W +
-                   i % (16 * W)] = from_f32<T>(0.f);
+    for (int64_t i = tid; i < (int64_t)sp.len * kCols; i += blockDim.x)
+      ((T *)a.out)[(sp.start + i / kCols) * a.out_stride + (int64_t)head * a.dv + slice * kCols + i % kCols] =
+          from_f32<T>(0.f);
     return;
   }
   const int64_t slot0 = (int64_t)(sp.start / C) + seq;
-  if (warp == W) {
+  if (warp == 2 * kChains) {
+    // ============================================================== copies
     if (lane == 0)
       for (int i = 0; i < n_chunks; ++i) {
         const int st = i % kStages;
-        if (i >= kStages && !ptx::mbar_wait_suspend(empty + st, ((i / kStages) & 1) ^ 1)) {
+        if (i >= kStages && !ptx::mbar_wait_suspend(bars->empty + st, ((i / kStages) & 1) ^ 1)) {
           set_status(a.status, REDLITE_STATUS_TIMEOUT);
           break;
         }
         uint8_t *dst = smem + st * kStage;
-        ptx::mbar_expect_tx(full + st, kStage);
+        ptx::mbar_expect_tx(bars->full + st, kStage);
         ptx::bulk_g2s(dst, a.ws + w.kq + ((size_t)(slot0 + i) * a.n_k + kh) * kq_bytes<NK, DK>(), kq_bytes<NK, DK>(),
-                      full + st);
+                      bars->full + st);
         ptx::bulk_g2s(dst + kq_bytes<NK, DK>(), a.ws + w.head + ((size_t)(slot0 + i) * a.n_v + head) * kHeadBlock,
-                      kHeadBlock, full + st);
+                      kHeadBlock, bars->full + st);
       }
     return;
   }
+  auto wait = [&](uint64_t *bar, uint32_t parity) {
+    const bool ok = __all_sync(0xffffffffu, ptx::mbar_wait_suspend(bar, parity));
+    if (!ok && lane == 0) set_status(a.status, REDLITE_STATUS_TIMEOUT);
+    return ok;
+  };
+  auto arrive = [&](uint64_t *bar) {
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(bar);
+  };
+  const int me = warp % kChains, col = slice * kCols + 8 * me;
+  Handoff<kLo> &ho = handoff[me];
+  T *const out = (T *)a.out + (int64_t)sp.start * a.out_stride + (int64_t)head * a.dv + col + 2 * c;
 
-  // ---- state: rows = value columns col + r, col + r + 8; columns = key index
-  const int col = slice * 16 * W + 16 * warp;
-  float S[NT][4];
-  const int64_t s_at = (slot * a.n_v + head) * (int64_t)DK * a.dv + col;
+  if (warp >= kChains) {
+    // ============================================== outputs: Q S + P D
+    for (int i = 0; i < n_chunks; ++i) {
+      const int st = i % kStages, n = min(C, sp.len - i * C);
+      const uint32_t sQ = ptx::smem_u32(smem + st * kStage) + NK * kTile;
+      const uint32_t sP = sQ + NK * kTile + kPhi * kPlane;
+      const float *f = reinterpret_cast<const float *>(smem + st * kStage + kq_bytes<NK, DK>() + kPlanes * kPlane);
+      if (!wait(bars->full + st, (i / kStages) & 1) || !wait(bars->s_ready + me, i & 1)) break;
+      float O[4][4];
+      zero(O);
+      const float2 u = ho.scale[c];
+#pragma unroll
+      for (int k2 = 0; k2 < NT / 2; ++k2) {
+        const uint4 h = ho.s[0][k2][lane];
+        uint4 l = h;
+        if (kLo) l = ho.s[kLo][k2][lane];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t h0 = e ? h.z : h.x, h1 = e ? h.w : h.y, l0 = e ? l.z : l.x, l1 = e ? l.w : l.y;
+          uint32_t q[4][4];
+          load_rows<DK>(sQ, 2 * k2 + e, lane, q);
+#pragma unroll
+          for (int t = 0; t < 4; ++t) mma_f16(O[t], q[t], h0, h1);
+          if (kLo)
+#pragma unroll
+            for (int t = 0; t < 4; ++t) mma_f16(O[t], q[t], l0, l1);
+          if (NK == 2) {
+            load_rows<DK>(sQ + kTile, 2 * k2 + e, lane, q);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) mma_f16(O[t], q[t], h0, h1);
+          }
+        }
+      }
+      arrive(bars->s_taken + me);
+      if (!wait(bars->d_ready + me, i & 1)) break;
+      float D[4][4], m0 = 0.f, m1 = 0.f;
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const float4 y = ho.d[t][lane];
+        D[t][0] = y.x, D[t][1] = y.y, D[t][2] = y.z, D[t][3] = y.w;
+        m0 = fmaxf(m0, fmaxf(fabsf(y.x), fabsf(y.z))), m1 = fmaxf(m1, fmaxf(fabsf(y.y), fabsf(y.w)));
+      }
+      const bool walk = ho.walk;
+      arrive(bars->d_taken + me);
+      if (!walk) {
+        col_max(m0, m1);
+        float i0, i1;
+        const float s0 = scale_f16(m0, i0), s1 = scale_f16(m1, i1);
+        uint32_t h[4][2], l[4][2];
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) split_tile(D[ks], s0, s1, h[ks], l[ks]);
+        triangle<kLo>(D, sP, h, l, lane);
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int j = 16 * t + 8 * e + r;
+            const float fq = f[fQ * C + j], fp = f[fP * C + j];
+            if (j < n)
+              store2<T>(out + (int64_t)(i * C + j) * a.out_stride, fmaf(D[t][2 * e] * fp, i0, O[t][2 * e] * u.x * fq),
+                        fmaf(D[t][2 * e + 1] * fp, i1, O[t][2 * e + 1] * u.y * fq));
+          }
+      }
+      arrive(bars->empty + st);
+    }
+    return;
+  }
+
+  // ================================================================ chain
+  // state: rows = keys 16 t + r, + 8; columns = value columns col + 2 c, + 1.
+  // The state is S * sg (a power of two per column).
+  float S[NT][4], sg0 = 1.f, sg1 = 1.f;
+  const int64_t s_at = ((slot * a.n_v + head) * (int64_t)DK + r) * a.dv + col + 2 * c;
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      S[t][e] = a.state_in
-                    ? __ldg(a.state_in + s_at + (int64_t)(8 * t + 2 * c + (e & 1)) * a.dv + r + 8 * (e >> 1))
-                    : 0.f;
-  // value rows of a chunk, this warp's 16 columns: asynchronous copies into a
-  // buffer of its own, zeros behind the end
-  constexpr int kPer = 16 * (int)sizeof(T) / 16;  // 16-byte pieces per row
-  constexpr int kPitch = VTile<T>::kPitch;
+    for (int e = 0; e < 2; ++e) {
+      float2 x = make_float2(0.f, 0.f);
+      if (a.state_in) x = __ldg(reinterpret_cast<const float2 *>(a.state_in + s_at + (int64_t)(16 * t + 8 * e) * a.dv));
+      S[t][2 * e] = x.x, S[t][2 * e + 1] = x.y;
+    }
+  // value rows of a chunk, this warp's eight columns: asynchronous copies into
+  // a buffer of its own, zeros behind the end
+  constexpr int kPer = 8 * (int)sizeof(T) / 16;  // 16-byte pieces per row
   auto fetch_v = [&](int i) {
-    const uint32_t dst = ptx::smem_u32(vbuf + (2 * warp + (i & 1)) * VTile<T>::kBytes);
+    const uint32_t dst = ptx::smem_u32(vbuf + (2 * me + (i & 1)) * Plan::kV);
     const int n = min(C, sp.len - i * C);
 #pragma unroll
     for (int it = 0; it < C * kPer / 32; ++it) {
       const int id = it * 32 + lane, row = id / kPer, piece = id % kPer;
       const T *src = (const T *)a.v + (int64_t)(sp.start + i * C + (row < n ? row : 0)) * a.v_stride +
                      (int64_t)head * a.dv + col + piece * (16 / (int)sizeof(T));
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                       dst + (uint32_t)(row * kPitch * (int)sizeof(T) + piece * 16)),
-                   "l"(src), "r"(row < n ? 16 : 0)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + (uint32_t)(id * 16)), "l"(src),
+                   "r"(row < n ? 16 : 0)
                    : "memory");
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -403,267 +739,212 @@ __global__ void __launch_bounds__(32 * (W + 1), 1) delta_chain_kernel(const Delt
 
   for (int i = 0; i < n_chunks; ++i) {
     const int st = i % kStages, n = min(C, sp.len - i * C);
-    const uint32_t sK = ptx::smem_u32(smem + st * kStage), sQ = sK + NK * kTile;
-    const uint32_t sT = sK + kq_bytes<NK, DK>(), sP = sT + kPhi * kPlane;
+    const uint32_t sK = ptx::smem_u32(smem + st * kStage), sT = sK + kq_bytes<NK, DK>();
     const float *f = reinterpret_cast<const float *>(smem + st * kStage + kq_bytes<NK, DK>() + kPlanes * kPlane);
-    T *vt = reinterpret_cast<T *>(vbuf + (2 * warp + (i & 1)) * VTile<T>::kBytes);
-    if (i + 1 < n_chunks) {
-      fetch_v(i + 1);
-      asm volatile("cp.async.wait_group 1;" ::: "memory");
-    } else {
-      asm volatile("cp.async.wait_group 0;" ::: "memory");
+    const T *vt = reinterpret_cast<const T *>(vbuf + (2 * me + (i & 1)) * Plan::kV);
+    // ---- the state in two parts
+    float sm0 = 0.f, sm1 = 0.f;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      sm0 = fmaxf(sm0, fmaxf(fabsf(S[t][0]), fabsf(S[t][2])));
+      sm1 = fmaxf(sm1, fmaxf(fabsf(S[t][1]), fabsf(S[t][3])));
     }
-    if (!__all_sync(0xffffffffu, ptx::mbar_wait_suspend(full + st, (i / kStages) & 1))) {
-      if (lane == 0) set_status(a.status, REDLITE_STATUS_TIMEOUT);
-      break;
+    col_max(sm0, sm1);
+    float u0, u1;
+    uint32_t sh[NT][2], sl[NT][2];
+    {
+      const float s0 = scale_f16(sm0, u0), s1 = scale_f16(sm1, u1);
+      u0 *= sg0, u1 *= sg1;
+#pragma unroll
+      for (int ks = 0; ks < NT; ++ks) split_tile(S[ks], s0, s1, sh[ks], sl[ks]);
     }
+    if (i + 1 < n_chunks) fetch_v(i + 1);
+    if (!wait(bars->full + st, (i / kStages) & 1)) break;
+    // ---- K S
+    float R[4][4], D[4][4];
+    zero(R);
+#pragma unroll
+    for (int ks = 0; ks < NT; ++ks) {
+      uint32_t k[4][4];
+      load_rows<DK>(sK, ks, lane, k);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) mma_f16(R[t], k[t], sh[ks][0], sh[ks][1]);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) mma_f16(R[t], k[t], sl[ks][0], sl[ks][1]);
+      if (NK == 2) {
+        load_rows<DK>(sK + kTile, ks, lane, k);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) mma_f16(R[t], k[t], sh[ks][0], sh[ks][1]);
+      }
+    }
+    // ---- the state's parts to the output warp, while the products run
+    if (i > 0 && !wait(bars->s_taken + me, (i - 1) & 1)) break;
+#pragma unroll
+    for (int k2 = 0; k2 < NT / 2; ++k2) {
+      ho.s[0][k2][lane] = make_uint4(sh[2 * k2][0], sh[2 * k2][1], sh[2 * k2 + 1][0], sh[2 * k2 + 1][1]);
+      if (kLo) ho.s[kLo][k2][lane] = make_uint4(sl[2 * k2][0], sl[2 * k2][1], sl[2 * k2 + 1][0], sl[2 * k2 + 1][1]);
+    }
+    if (r == 0) ho.scale[c] = make_float2(u0, u1);
+    arrive(bars->s_ready + me);
+    if (i + 1 < n_chunks) asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncwarp();
-    float R[8][4], O[8][4];
+    // ---- beta V - beta exp(c) K S
+    float m0 = 0.f, m1 = 0.f;
 #pragma unroll
-    for (int t = 0; t < 8; ++t)
+    for (int t = 0; t < 4; ++t)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) R[t][e] = O[t][e] = 0.f;
-    // ---- S^T K^T and S^T Q^T
+      for (int e = 0; e < 2; ++e) {
+        const int j = 16 * t + 8 * e + r;
+        const float2 v = load2(vt + j * 8 + 2 * c);
+        const float fb = f[fBeta * C + j], fr = f[fR * C + j];
+        R[t][2 * e] = fmaf(fb, v.x, -fr * (R[t][2 * e] * u0));
+        R[t][2 * e + 1] = fmaf(fb, v.y, -fr * (R[t][2 * e + 1] * u1));
+        m0 = fmaxf(m0, fabsf(R[t][2 * e])), m1 = fmaxf(m1, fabsf(R[t][2 * e + 1]));
+      }
+    col_max(m0, m1);
+    uint32_t h[4][2], l[4][2];
+    float i0, i1, odd = 0.f;  // odd: a NaN or an infinity anywhere (x - x is not 0)
+    {
+      const float s0 = scale_f16(m0, i0), s1 = scale_f16(m1, i1);
 #pragma unroll
-    for (int ks = 0; ks < DK / 16; ++ks) {
-      uint32_t h[4], l[4];
-      split_bf16(S[2 * ks][0], S[2 * ks][1], h[0], l[0]);
-      split_bf16(S[2 * ks][2], S[2 * ks][3], h[1], l[1]);
-      split_bf16(S[2 * ks + 1][0], S[2 * ks + 1][1], h[2], l[2]);
-      split_bf16(S[2 * ks + 1][2], S[2 * ks + 1][3], h[3], l[3]);
+      for (int ks = 0; ks < 4; ++ks) split_tile(R[ks], s0, s1, h[ks], l[ks]);
+    }
+    // ---- D = T R
+    triangle<true>(D, sT, h, l, lane);
+    const float last = f[fLast * C];
+    m0 = last * sm0 * sg0 * 0x1p-60f, m1 = last * sm1 * sg1 * 0x1p-60f;
+    if (i > 0 && !wait(bars->d_taken + me, (i - 1) & 1)) break;
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const uint32_t off = kq_off<DK>(16 * t + (lane & 7) + ((lane >> 4) << 3), 2 * ks + ((lane >> 3) & 1));
+    for (int t = 0; t < 4; ++t) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float ft = f[fT * C + 16 * t + 8 * e + r];
+        D[t][2 * e] *= ft * i0, D[t][2 * e + 1] *= ft * i1;
+        odd += (D[t][2 * e] - D[t][2 * e]) + (D[t][2 * e + 1] - D[t][2 * e + 1]);
+      }
+      ho.d[t][lane] = make_float4(D[t][0], D[t][1], D[t][2], D[t][3]);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float fk = f[fK * C + 16 * t + 8 * e + r];
+        D[t][2 * e] *= fk, D[t][2 * e + 1] *= fk;
+        m0 = fmaxf(m0, fabsf(D[t][2 * e])), m1 = fmaxf(m1, fabsf(D[t][2 * e + 1]));
+      }
+    }
+    const bool walk = __any_sync(0xffffffffu, !(odd == 0.f));
+    if (lane == 0) ho.walk = walk;
+    arrive(bars->d_ready + me);
+    if (!walk) {
+      // ---- S = exp(c_last) S + K^T (exp(c_last - c) D), on the scale of the
+      // updates (or of what is left of the state, if that is 2^60 larger)
+      col_max(m0, m1);
+      const float s0 = scale_f16(m0, i0), s1 = scale_f16(m1, i1), f0 = last * sg0 * s0, f1 = last * sg1 * s1;
+      sg0 = i0, sg1 = i1;
+#pragma unroll
+      for (int t = 0; t < NT; ++t) S[t][0] *= f0, S[t][1] *= f1, S[t][2] *= f0, S[t][3] *= f1;
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks) split_tile(D[ks], s0, s1, h[ks], l[ks]);
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks)
 #pragma unroll
         for (int p = 0; p < NK; ++p) {
-          uint32_t b[4], d[4];
-          ldsm4(sK + p * kTile + off, b[0], b[1], b[2], b[3]);
-          ldsm4(sQ + p * kTile + off, d[0], d[1], d[2], d[3]);
+          uint32_t k[NT][4];
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            mma_bf16(R[2 * t + u], h[0], h[1], h[2], h[3], b[2 * u], b[2 * u + 1]);
-            mma_bf16(O[2 * t + u], h[0], h[1], h[2], h[3], d[2 * u], d[2 * u + 1]);
-            if (p == 0) {
-              mma_bf16(R[2 * t + u], l[0], l[1], l[2], l[3], b[2 * u], b[2 * u + 1]);
-              mma_bf16(O[2 * t + u], l[0], l[1], l[2], l[3], d[2 * u], d[2 * u + 1]);
-            }
-          }
+          for (int t = 0; t < NT; ++t)
+            ldsm4t(sK + p * kTile + kq_off<DK>(16 * ks + (lane & 7) + ((lane >> 4) << 3), 2 * t + ((lane >> 3) & 1)),
+                   k[t][0], k[t][1], k[t][2], k[t][3]);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) mma_f16(S[t], k[t], h[ks][0], h[ks][1]);
+          if (p == 0)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) mma_f16(S[t], k[t], l[ks][0], l[ks][1]);
         }
-      }
-    }
-    // ---- beta V - beta exp(c) K S0, and the state's part of the output
-#pragma unroll
-    for (int t = 0; t < 8; ++t) {
-      const int j = 8 * t + 2 * c;
-      const float2 fb = *reinterpret_cast<const float2 *>(f + fBeta * C + j);
-      const float2 fr = *reinterpret_cast<const float2 *>(f + fR * C + j);
-      const float2 fq = *reinterpret_cast<const float2 *>(f + fQ * C + j);
-      R[t][0] = fmaf(fb.x, to_f32(vt[j * kPitch + r]), -fr.x * R[t][0]);
-      R[t][1] = fmaf(fb.y, to_f32(vt[(j + 1) * kPitch + r]), -fr.y * R[t][1]);
-      R[t][2] = fmaf(fb.x, to_f32(vt[j * kPitch + r + 8]), -fr.x * R[t][2]);
-      R[t][3] = fmaf(fb.y, to_f32(vt[(j + 1) * kPitch + r + 8]), -fr.y * R[t][3]);
-      O[t][0] *= fq.x, O[t][1] *= fq.y, O[t][2] *= fq.x, O[t][3] *= fq.y;
-    }
-    // ---- D^T = R^T T^T (T is lower triangular: 10 of 16 blocks)
-    float D[8][4];
-#pragma unroll
-    for (int t = 0; t < 8; ++t)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) D[t][e] = 0.f;
-#pragma unroll
-    for (int ks = 0; ks < 4; ++ks) {
-      uint32_t h[4], l[4];
-      split_bf16(R[2 * ks][0], R[2 * ks][1], h[0], l[0]);
-      split_bf16(R[2 * ks][2], R[2 * ks][3], h[1], l[1]);
-      split_bf16(R[2 * ks + 1][0], R[2 * ks + 1][1], h[2], l[2]);
-      split_bf16(R[2 * ks + 1][2], R[2 * ks + 1][3], h[3], l[3]);
-#pragma unroll
-      for (int t = ks; t < 4; ++t) {
-        const uint32_t off = tp_off(16 * t + (lane & 7) + ((lane >> 4) << 3), 2 * ks + ((lane >> 3) & 1));
-        uint32_t b[4], d[4];
-        ldsm4(sT + kThi * kPlane + off, b[0], b[1], b[2], b[3]);
-        ldsm4(sT + kTlo * kPlane + off, d[0], d[1], d[2], d[3]);
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          mma_bf16(D[2 * t + u], h[0], h[1], h[2], h[3], b[2 * u], b[2 * u + 1]);
-          mma_bf16(D[2 * t + u], l[0], l[1], l[2], l[3], b[2 * u], b[2 * u + 1]);
-          mma_bf16(D[2 * t + u], h[0], h[1], h[2], h[3], d[2 * u], d[2 * u + 1]);
-        }
-      }
-    }
-    // a NaN or an infinity anywhere: x - x is not 0
-    float odd = 0.f;
-#pragma unroll
-    for (int t = 0; t < 8; ++t)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) odd += D[t][e] - D[t][e];
-    const bool walk = __any_sync(0xffffffffu, !(odd == 0.f));
-    __syncwarp();  // V is read: its buffer takes the outputs
-    if (!walk) {
-      const float last = f[fLast * C];
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) S[t][e] *= last;
-      // ---- O^T += D^T P^T,  S^T += (D exp(c_last - c))^T K
-#pragma unroll
-      for (int ks = 0; ks < 4; ++ks) {
-        uint32_t h[4], l[4];
-        split_bf16(D[2 * ks][0], D[2 * ks][1], h[0], l[0]);
-        split_bf16(D[2 * ks][2], D[2 * ks][3], h[1], l[1]);
-        split_bf16(D[2 * ks + 1][0], D[2 * ks + 1][1], h[2], l[2]);
-        split_bf16(D[2 * ks + 1][2], D[2 * ks + 1][3], h[3], l[3]);
-#pragma unroll
-        for (int t = ks; t < 4; ++t) {
-          const uint32_t off = tp_off(16 * t + (lane & 7) + ((lane >> 4) << 3), 2 * ks + ((lane >> 3) & 1));
-          uint32_t b[4], d[4];
-          ldsm4(sP + off, b[0], b[1], b[2], b[3]);
-          ldsm4(sP + kPlane + off, d[0], d[1], d[2], d[3]);
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            mma_bf16(O[2 * t + u], h[0], h[1], h[2], h[3], b[2 * u], b[2 * u + 1]);
-            mma_bf16(O[2 * t + u], l[0], l[1], l[2], l[3], b[2 * u], b[2 * u + 1]);
-            mma_bf16(O[2 * t + u], h[0], h[1], h[2], h[3], d[2 * u], d[2 * u + 1]);
-          }
-        }
-        const float2 f0 = *reinterpret_cast<const float2 *>(f + fK * C + 16 * ks + 2 * c);
-        const float2 f1 = *reinterpret_cast<const float2 *>(f + fK * C + 16 * ks + 8 + 2 * c);
-        split_bf16(D[2 * ks][0] * f0.x, D[2 * ks][1] * f0.y, h[0], l[0]);
-        split_bf16(D[2 * ks][2] * f0.x, D[2 * ks][3] * f0.y, h[1], l[1]);
-        split_bf16(D[2 * ks + 1][0] * f1.x, D[2 * ks + 1][1] * f1.y, h[2], l[2]);
-        split_bf16(D[2 * ks + 1][2] * f1.x, D[2 * ks + 1][3] * f1.y, h[3], l[3]);
-#pragma unroll
-        for (int t = 0; t < NT / 2; ++t) {
-          const uint32_t off = kq_off<DK>(16 * ks + (lane & 15), 2 * t + (lane >> 4));
-#pragma unroll
-          for (int p = 0; p < NK; ++p) {
-            uint32_t b[4];
-            ldsm4t(sK + p * kTile + off, b[0], b[1], b[2], b[3]);
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              mma_bf16(S[2 * t + u], h[0], h[1], h[2], h[3], b[2 * u], b[2 * u + 1]);
-              if (p == 0) mma_bf16(S[2 * t + u], l[0], l[1], l[2], l[3], b[2 * u], b[2 * u + 1]);
-            }
-          }
-        }
-      }
-#pragma unroll
-      for (int t = 0; t < 8; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          vt[(8 * t + 2 * c + (e & 1)) * kPitch + r + 8 * (e >> 1)] = from_f32<T>(O[t][e]);
     } else {
       // token by token from the state in front of the chunk
+#pragma unroll
+      for (int t = 0; t < NT; ++t) S[t][0] *= sg0, S[t][1] *= sg1, S[t][2] *= sg0, S[t][3] *= sg1;
+      sg0 = sg1 = 1.f;
+      auto total = [&](float &p0, float &p1) {
+#pragma unroll
+        for (int o = 4; o <= 16; o <<= 1) {
+          p0 += __shfl_xor_sync(0xffffffffu, p0, o);
+          p1 += __shfl_xor_sync(0xffffffffu, p1, o);
+        }
+      };
+      auto value = [&](uint32_t tile, int j, int key) {  // the parts of one key's element
+        float v = 0.f;
+#pragma unroll
+        for (int p = 0; p < NK; ++p)
+          v += __half2float(__ushort_as_half(
+              (uint16_t)ptx::lds16(tile + p * kTile + kq_off<DK>(j, key >> 3) + 2 * (key & 7))));
+        return v;
+      };
       for (int j = 0; j < n; ++j) {
-        float ks0 = 0.f, ks1 = 0.f;
         const float al = f[fAlpha * C + j], be = f[fBeta * C + j], nk = f[fNk * C + j], nq = f[fNq * C + j];
+        float p0 = 0.f, p1 = 0.f;
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          float2 k = make_float2(0.f, 0.f);
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
-          for (int p = 0; p < NK; ++p) {
-            const uint32_t x = ptx::lds32(sK + p * kTile + kq_off<DK>(j, t) + 4 * c);
-            k.x += bf16_lo(x), k.y += bf16_hi(x);
+          for (int e = 0; e < 2; ++e) {
+            const float k = value(sK, j, 16 * t + 8 * e + r);
+            p0 = fmaf(k, S[t][2 * e], p0), p1 = fmaf(k, S[t][2 * e + 1], p1);
           }
-          ks0 = fmaf(k.x, S[t][0], fmaf(k.y, S[t][1], ks0));
-          ks1 = fmaf(k.x, S[t][2], fmaf(k.y, S[t][3], ks1));
-        }
+        total(p0, p1);
+        const float2 v = load2(vt + j * 8 + 2 * c);
+        const float d0 = be * (v.x - al * nk * p0) * nk, d1 = be * (v.y - al * nk * p1) * nk;
+        p0 = p1 = 0.f;
 #pragma unroll
-        for (int o = 1; o <= 2; o <<= 1) {
-          ks0 += __shfl_xor_sync(0xffffffffu, ks0, o);
-          ks1 += __shfl_xor_sync(0xffffffffu, ks1, o);
-        }
-        const float d0 = be * (to_f32(vt[j * kPitch + r]) - al * nk * ks0) * nk;
-        const float d1 = be * (to_f32(vt[j * kPitch + r + 8]) - al * nk * ks1) * nk;
-        float o0 = 0.f, o1 = 0.f;
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          float2 k = make_float2(0.f, 0.f), q = k;
-#pragma unroll
-          for (int p = 0; p < NK; ++p) {
-            const uint32_t x = ptx::lds32(sK + p * kTile + kq_off<DK>(j, t) + 4 * c);
-            const uint32_t y = ptx::lds32(sQ + p * kTile + kq_off<DK>(j, t) + 4 * c);
-            k.x += bf16_lo(x), k.y += bf16_hi(x), q.x += bf16_lo(y), q.y += bf16_hi(y);
+          for (int e = 0; e < 2; ++e) {
+            const float k = value(sK, j, 16 * t + 8 * e + r), q = value(sK + NK * kTile, j, 16 * t + 8 * e + r);
+            S[t][2 * e] = fmaf(al, S[t][2 * e], k * d0), S[t][2 * e + 1] = fmaf(al, S[t][2 * e + 1], k * d1);
+            p0 = fmaf(q, S[t][2 * e], p0), p1 = fmaf(q, S[t][2 * e + 1], p1);
           }
-          S[t][0] = fmaf(al, S[t][0], k.x * d0), S[t][1] = fmaf(al, S[t][1], k.y * d0);
-          S[t][2] = fmaf(al, S[t][2], k.x * d1), S[t][3] = fmaf(al, S[t][3], k.y * d1);
-          o0 = fmaf(q.x, S[t][0], fmaf(q.y, S[t][1], o0));
-          o1 = fmaf(q.x, S[t][2], fmaf(q.y, S[t][3], o1));
-        }
-#pragma unroll
-        for (int o = 1; o <= 2; o <<= 1) {
-          o0 += __shfl_xor_sync(0xffffffffu, o0, o);
-          o1 += __shfl_xor_sync(0xffffffffu, o1, o);
-        }
-        __syncwarp();
-        if (c == 0) vt[j * kPitch + r] = from_f32<T>(o0 * nq), vt[j * kPitch + r + 8] = from_f32<T>(o1 * nq);
-        __syncwarp();
+        total(p0, p1);
+        if (r == 0) store2<T>(out + (int64_t)(i * C + j) * a.out_stride, p0 * nq, p1 * nq);
       }
     }
-    // ---- the stage is free; outputs leave as 16-byte pieces of rows
-    ptx::fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) ptx::mbar_arrive(empty + st);
-#pragma unroll
-    for (int it = 0; it < C * kPer / 32; ++it) {
-      const int id = it * 32 + lane, row = id / kPer, piece = id % kPer;
-      if (row < n) {
-        const uint4 v = *reinterpret_cast<const uint4 *>(reinterpret_cast<const uint8_t *>(vt) +
-                                                         row * kPitch * (int)sizeof(T) + piece * 16);
-        *reinterpret_cast<uint4 *>((T *)a.out + (int64_t)(sp.start + i * C + row) * a.out_stride +
-                                   (int64_t)head * a.dv + col + piece * (16 / (int)sizeof(T))) = v;
-      }
-    }
-    __syncwarp();  // the buffer is read before the copies of the chunk after next go into it
+    arrive(bars->empty + st);
   }
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      a.state_out[s_at + (int64_t)(8 * t + 2 * c + (e & 1)) * a.dv + r + 8 * (e >> 1)] = S[t][e];
+    for (int e = 0; e < 2; ++e)
+      *reinterpret_cast<float2 *>(a.state_out + s_at + (int64_t)(16 * t + 8 * e) * a.dv) =
+          make_float2(S[t][2 * e] * sg0, S[t][2 * e + 1] * sg1);
 }
 
-template <typename T, int NK, int DK, int W>
-cudaError_t launch_chain(const DeltaArgs &a, const WsPlan &w, cudaStream_t s) {
-  constexpr int smem = chain_smem<T, NK, DK, W>();
-  static_assert(smem <= 227 * 1024, "shared memory of a chain block");
-  cudaError_t e = cudaFuncSetAttribute(delta_chain_kernel<T, NK, DK, W>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       smem);
+template <typename T, int NK, int DK>
+cudaError_t launch_prefill(const DeltaArgs &a, const WsPlan &w, cudaStream_t s) {
+  cudaError_t e;
+  if (a.n_tokens > 0) {
+    constexpr int smem = prep_smem<NK, DK>();
+    e = cudaFuncSetAttribute(delta_prep_kernel<T, NK, DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    delta_prep_kernel<T, NK, DK>
+        <<<dim3((unsigned)chunk_slots(a.n_tokens, a.n_seqs), (unsigned)a.n_k), 256, smem, s>>>(a, w);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  constexpr int smem = Chain<T, NK, DK>::kSmem;
+  e = cudaFuncSetAttribute(delta_chain_kernel<T, NK, DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((int64_t)a.n_seqs * a.n_v * (a.dv / (16 * W))));
-  cfg.blockDim = dim3(32 * (W + 1));
+  cfg.gridDim = dim3((unsigned)((int64_t)a.n_seqs * a.n_v * (a.dv / kCols)));
+  cfg.blockDim = dim3(32 * (2 * kChains + 1));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at, cfg.numAttrs = a.n_tokens > 0 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, delta_chain_kernel<T, NK, DK, W>, a, w);
-}
-
-template <typename T, int NK, int DK>
-cudaError_t launch_prefill(const DeltaArgs &a, const WsPlan &w, int sms, cudaStream_t s) {
-  if (a.n_tokens > 0) {
-    constexpr int tiles = kq_bytes<NK, DK>(), at = 2 * C * 68 * 4, smem = tiles > at ? tiles : at;
-    cudaError_t e =
-        cudaFuncSetAttribute(delta_prep_kernel<T, NK, DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    delta_prep_kernel<T, NK, DK>
-        <<<dim3((unsigned)chunk_slots(a.n_tokens, a.n_seqs), (unsigned)a.n_k), 128, smem, s>>>(a, w);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-  }
-  // two warps per block while that does not make more blocks than there are
-  // multiprocessors (a chain is serial: spread the few there are), else four
-  const int64_t chains = (int64_t)a.n_seqs * a.n_v * (a.dv / 32);
-  if (chains <= sms) return launch_chain<T, NK, DK, 2>(a, w, s);
-  return launch_chain<T, NK, DK, 4>(a, w, s);
+  return cudaLaunchKernelEx(&cfg, delta_chain_kernel<T, NK, DK>, a, w, a.n_tokens > 0);
 }
 
 template <typename T, int NK>
-cudaError_t launch_prefill_dk(const DeltaArgs &a, const WsPlan &w, int sms, cudaStream_t s) {
-  return a.dk == 128 ? launch_prefill<T, NK, 128>(a, w, sms, s) : launch_prefill<T, NK, 64>(a, w, sms, s);
+cudaError_t launch_prefill_dk(const DeltaArgs &a, const WsPlan &w, cudaStream_t s) {
+  return a.dk == 128 ? launch_prefill<T, NK, 128>(a, w, s) : launch_prefill<T, NK, 64>(a, w, s);
 }
 
 }  // namespace
@@ -676,7 +957,7 @@ extern "C" size_t redlite_delta_workspace_bytes(int32_t n_tokens, int32_t n_seqs
   if (n_tokens < 0 || n_seqs < 0 || n_k_heads < 1 || n_v_heads < 1 || n_v_heads > 1024 || n_v_heads % n_k_heads)
     return 0;
   if ((dk != 64 && dk != 128) || (dv != 64 && dv != 128)) return 0;
-  return ws_plan(chunk_slots(n_tokens, n_seqs), n_k_heads, n_v_heads, dk).total;
+  return ws_plan(chunk_slots(n_tokens, n_seqs), n_seqs, n_k_heads, n_v_heads, dk).total;
 }
 
 extern "C" int redlite_delta_prefill(int32_t dtype, const void *q, int64_t q_stride, const void *k, int64_t k_stride,
@@ -691,12 +972,10 @@ extern "C" int redlite_delta_prefill(int32_t dtype, const void *q, int64_t q_str
   if (rc <= 0) return rc;
   if (!cu || !workspace || ((uintptr_t)workspace & 255)) return REDLITE_EINVAL;
   const int64_t slots_n = chunk_slots(n_tokens, n_seqs);
-  if ((int64_t)n_seqs * n_v_heads * (dv / 32) >= ((int64_t)1 << 31) - 1 || slots_n >= ((int64_t)1 << 31) - 1)
+  if ((int64_t)n_seqs * n_v_heads * (dv / kCols) >= ((int64_t)1 << 31) - 1 || slots_n >= ((int64_t)1 << 31) - 1)
     return REDLITE_EUNSUPPORTED;
-  const WsPlan w = ws_plan(slots_n, n_k_heads, n_v_heads, dk);
+  const WsPlan w = ws_plan(slots_n, n_seqs, n_k_heads, n_v_heads, dk);
   if (workspace_bytes < w.total) return REDLITE_ENOMEM;
-  const int sms = sm_count();
-  if (sms <= 0) return REDLITE_ECUDA;
   DeltaArgs a = {};
   a.q = q, a.k = k, a.v = v, a.q_stride = q_stride, a.k_stride = k_stride, a.v_stride = v_stride;
   a.out_stride = out_stride, a.g = g, a.beta = beta, a.cu = cu, a.slots = slots;
@@ -705,9 +984,9 @@ extern "C" int redlite_delta_prefill(int32_t dtype, const void *q, int64_t q_str
   a.out = out, a.ws = (uint8_t *)workspace, a.status = status;
   cudaStream_t s = (cudaStream_t)stream;
   cudaError_t e;
-  // fp16 keys and queries are held exactly by two bf16 parts, fp32 ones to 2^-17
-  if (dtype == REDLITE_T_F32) e = launch_prefill_dk<float, 2>(a, w, sms, s);
-  else if (dtype == REDLITE_T_BF16) e = launch_prefill_dk<__nv_bfloat16, 1>(a, w, sms, s);
-  else e = launch_prefill_dk<__half, 2>(a, w, sms, s);
+  // 16-bit keys and queries are one fp16 part (exact once scaled), fp32 ones two
+  if (dtype == REDLITE_T_F32) e = launch_prefill_dk<float, 2>(a, w, s);
+  else if (dtype == REDLITE_T_BF16) e = launch_prefill_dk<__nv_bfloat16, 1>(a, w, s);
+  else e = launch_prefill_dk<__half, 1>(a, w, s);
   return e == cudaSuccess ? REDLITE_OK : REDLITE_ECUDA;
 }

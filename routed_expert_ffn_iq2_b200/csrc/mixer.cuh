@@ -92,6 +92,22 @@ __device__ __forceinline__ void split_bf16(float a, float b, uint32_t &hi, uint3
   lo = pack_bf16(a - bf16_lo(hi), b - bf16_hi(hi));
 }
 
+// x = hi + lo with hi, lo in fp16, for values below 2^15: what is left out is
+// at most 2^-23 of x, or 2^-25 where x is small (fp16's smallest step).
+__device__ __forceinline__ void split_f16(float a, float b, uint32_t &hi, uint32_t &lo) {
+  hi = pack_f16(a, b);
+  const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+  lo = pack_f16(a - f.x, b - f.y);
+}
+// The power of two that takes m >= 0 into [2^14, 2^15) (2^126 at most), and
+// its inverse: a row so scaled and split in two fp16 parts is held to 2^-23 of
+// each element and 2^-39 of the row's largest.
+__device__ __forceinline__ float scale_f16(float m, float &inv) {
+  const int e = max(__float_as_int(m) >> 23, 15);
+  inv = __int_as_float((e - 14) << 23);
+  return __int_as_float((268 - e) << 23);
+}
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -106,6 +122,25 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// D[16x8] += A[16x8] B[8x8], tf32 in (the low 13 bits of an operand are not read).
+__device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// x = hi + lo, hi the nearest tf32 number: lo has 12 significant bits, of
+// which the product reads 11 (2^-22 of x is left out).
+__device__ __forceinline__ void split_tf32(float x, uint32_t &hi, uint32_t &lo) {
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(x));
+  lo = __float_as_uint(x - __uint_as_float(hi));
+}
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t &a, uint32_t &b, uint32_t &c, uint32_t &d) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(a), "=r"(b), "=r"(c), "=r"(d)
@@ -117,6 +152,13 @@ __device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t &a, uint32_t &b, 
                : "=r"(a), "=r"(b), "=r"(c), "=r"(d)
                : "r"(addr)
                : "memory");
+}
+
+// An 8 x 8 matrix of 16-bit values, one row per four lanes, transposed.
+__device__ __forceinline__ uint32_t movm(uint32_t v) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
 }
 
 __device__ __forceinline__ void set_status(int32_t *status, int bits) {
