@@ -200,14 +200,15 @@ __global__ void __launch_bounds__(256, 2) delta_prep_kernel(const DeltaArgs a, c
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ double tail[2];
   __shared__ float2 sc[2][C];  // sums of log2 decays: high and low part
-  __shared__ float snk[C], snq[C], sb[2][C];
+  __shared__ float snk[C], snq[C], sss[2][C], sb[2][C];
   __shared__ __align__(16) float td[2][4][16 * kPitchT];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, c = lane & 3;
-  if (blockIdx.x == 0 && blockIdx.y == 0)
+  if (blockIdx.x == 0)
     order_sequences(a, reinterpret_cast<int32_t *>(a.ws + w.order), reinterpret_cast<int *>(smem));
-  const int64_t slot = blockIdx.x;
-  const int kh = blockIdx.y, role = (warp + blockIdx.x) & 3, group = warp >> 2;
+  // key heads next to each other: blocks that run together read whole rows
+  const int64_t slot = blockIdx.x / a.n_k;
+  const int kh = blockIdx.x % a.n_k, role = (warp + blockIdx.x) & 3, group = warp >> 2;
   // the last sequence whose first slot is not behind this one
   int lo = 0, hi = a.n_seqs;
   while (hi - lo > 1) {
@@ -223,30 +224,42 @@ __global__ void __launch_bounds__(256, 2) delta_prep_kernel(const DeltaArgs a, c
   __syncthreads();
 
   // ---- K and Q rows: scaled fp16 parts into shared memory and the workspace,
-  // sums of squares; four pieces of a thread are on their way at a time
-  constexpr int kPieces = DK / 8, kTile = C * DK * 2, kRounds = 2 * C * kPieces / 256, kAhead = 4;
+  // sums of squares; a thread has several pieces on their way at a time
+  const int per = a.n_v / a.n_k, half = tid >> 6, tok = tid & 63;
+  float next_g, next_b;  // of this thread's token and head of a pair, on their way
+  auto fetch_gb = [&](int h0) {
+    next_g = next_b = 0.f;
+    if (half < 2 && h0 + half < per && tok < n) {
+      next_g = __ldg(a.g + (row0 + tok) * a.n_v + kh * per + h0 + half);
+      next_b = __ldg(a.beta + (row0 + tok) * a.n_v + kh * per + h0 + half);
+    }
+  };
+  fetch_gb(0);
+  constexpr int kPieces = DK / 8, kTile = C * DK * 2, kRounds = 2 * C * kPieces / 256, kAhead = NK == 1 ? kRounds : 4;
   uint8_t *kq = a.ws + w.kq + ((size_t)slot * a.n_k + kh) * kq_bytes<NK, DK>();
 #pragma unroll 1
   for (int r0 = 0; r0 < kRounds; r0 += kAhead) {
-    float x[kAhead][8];
+    constexpr int kLoads = (int)sizeof(T) / 2;
+    uint4 raw[kAhead][kLoads];
 #pragma unroll
     for (int it = 0; it < kAhead; ++it) {
       const int id = (r0 + it) * 256 + tid, which = id / (C * kPieces), row = id / kPieces % C, piece = id % kPieces;
-      if (row < n) {
-        load8<T>((which ? (const T *)a.q + (row0 + row) * a.q_stride : (const T *)a.k + (row0 + row) * a.k_stride) +
-                     (int64_t)kh * DK + piece * 8,
-                 x[it]);
-      } else {
+      const T *src = (which ? (const T *)a.q + (row0 + row) * a.q_stride : (const T *)a.k + (row0 + row) * a.k_stride) +
+                     (int64_t)kh * DK + piece * 8;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[it][e] = 0.f;
+      for (int e = 0; e < kLoads; ++e) {
+        raw[it][e] = make_uint4(0u, 0u, 0u, 0u);
+        if (row < n) raw[it][e] = __ldg(reinterpret_cast<const uint4 *>(src) + e);
       }
     }
 #pragma unroll
     for (int it = 0; it < kAhead; ++it) {
       const int id = (r0 + it) * 256 + tid, which = id / (C * kPieces), row = id / kPieces % C, piece = id % kPieces;
-      float ss = 0.f, mx = 0.f;
+      float ss = 0.f, mx = 0.f, x[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(x[it][e], x[it][e], ss), mx = fmaxf(mx, fabsf(x[it][e]));
+      for (int e = 0; e < 8; ++e) x[e] = to_f32(reinterpret_cast<const T *>(raw[it])[e]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss), mx = fmaxf(mx, fabsf(x[e]));
 #pragma unroll
       for (int o = 1; o < kPieces; o <<= 1) {
         ss += __shfl_xor_sync(0xffffffffu, ss, o);
@@ -254,15 +267,12 @@ __global__ void __launch_bounds__(256, 2) delta_prep_kernel(const DeltaArgs a, c
       }
       float inv;
       const float s = scale_f16(mx, inv);
-      if (piece == 0) {
-        const float f = a.qk_eps >= 0.f && row < n ? 1.f / sqrtf(ss + a.qk_eps) : 1.f;
-        (which ? snq : snk)[row] = f * inv;
-      }
+      if (piece == 0) (which ? snq : snk)[row] = inv, sss[which][row] = ss;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[it][e] *= s;
+      for (int e = 0; e < 8; ++e) x[e] *= s;
       uint4 v, u;
-      split_f16(x[it][0], x[it][1], v.x, u.x), split_f16(x[it][2], x[it][3], v.y, u.y);
-      split_f16(x[it][4], x[it][5], v.z, u.z), split_f16(x[it][6], x[it][7], v.w, u.w);
+      split_f16(x[0], x[1], v.x, u.x), split_f16(x[2], x[3], v.y, u.y);
+      split_f16(x[4], x[5], v.z, u.z), split_f16(x[6], x[7], v.w, u.w);
       const uint32_t off = which * NK * kTile + kq_off<DK>(row, piece);
       *reinterpret_cast<uint4 *>(smem + off) = v;
       *reinterpret_cast<uint4 *>(kq + off) = v;
@@ -273,6 +283,9 @@ __global__ void __launch_bounds__(256, 2) delta_prep_kernel(const DeltaArgs a, c
     }
   }
   __syncthreads();
+  if (tid < 2 * C && a.qk_eps >= 0.f && (tid & (C - 1)) < n) {  // read behind the barriers below
+    (tid < C ? snk : snq)[tid & (C - 1)] *= 1.f / sqrtf(sss[tid / C][tid & (C - 1)] + a.qk_eps);
+  }
   // ---- rows 16 role .. of K K^T (first group) or Q K^T
   float G[8][4];
 #pragma unroll
@@ -303,17 +316,13 @@ __global__ void __launch_bounds__(256, 2) delta_prep_kernel(const DeltaArgs a, c
     }
   }
   float *sa = reinterpret_cast<float *>(smem);  // A of two heads (the tiles are read)
-  const int per = a.n_v / a.n_k;
   for (int h0 = 0; h0 < per; h0 += 2) {
     __syncthreads();
     // ---- factors per token: of the first four warps, two take a head
-    const int half = tid >> 6, tok = tid & 63, head = kh * per + h0 + half;
+    const int head = kh * per + h0 + half;
     const bool have = half < 2 && h0 + half < per;
-    float g = 0.f, b = 0.f;
-    if (have && tok < n) {
-      g = delta_clamp_g(__ldg(a.g + (row0 + tok) * a.n_v + head));
-      b = __ldg(a.beta + (row0 + tok) * a.n_v + head);
-    }
+    const float g = delta_clamp_g(next_g), b = next_b;
+    fetch_gb(h0 + 2);
     double sum = g;
     if (half < 2) {
 #pragma unroll
@@ -923,7 +932,7 @@ cudaError_t launch_prefill(const DeltaArgs &a, const WsPlan &w, cudaStream_t s) 
     e = cudaFuncSetAttribute(delta_prep_kernel<T, NK, DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     delta_prep_kernel<T, NK, DK>
-        <<<dim3((unsigned)chunk_slots(a.n_tokens, a.n_seqs), (unsigned)a.n_k), 256, smem, s>>>(a, w);
+        <<<(unsigned)(chunk_slots(a.n_tokens, a.n_seqs) * a.n_k), 256, smem, s>>>(a, w);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
@@ -972,7 +981,7 @@ extern "C" int redlite_delta_prefill(int32_t dtype, const void *q, int64_t q_str
   if (rc <= 0) return rc;
   if (!cu || !workspace || ((uintptr_t)workspace & 255)) return REDLITE_EINVAL;
   const int64_t slots_n = chunk_slots(n_tokens, n_seqs);
-  if ((int64_t)n_seqs * n_v_heads * (dv / kCols) >= ((int64_t)1 << 31) - 1 || slots_n >= ((int64_t)1 << 31) - 1)
+  if ((int64_t)n_seqs * n_v_heads * (dv / kCols) >= ((int64_t)1 << 31) - 1 || slots_n * n_k_heads >= ((int64_t)1 << 31) - 1)
     return REDLITE_EUNSUPPORTED;
   const WsPlan w = ws_plan(slots_n, n_seqs, n_k_heads, n_v_heads, dk);
   if (workspace_bytes < w.total) return REDLITE_ENOMEM;
