@@ -4,12 +4,14 @@
 // full-attention parity", section "Pinned full-attention graph": grouped
 // heads over a K/V cache.)
 //
-// Both kernels move bytes: a thread owns eight consecutive values of one
-// token's head (one 32-bit code word), four threads a group of 32, so a
-// group's minimum and maximum are two shuffles, every load and store of
-// values is 16 bytes or more per thread, and no two tokens share a stored
-// byte (no read-modify-write between threads).  Bound by the bytes of the
-// unpacked side.
+// Both kernels move bytes: a thread owns eight consecutive values (one 32-bit
+// code word) of a token's head, of the key and of the value, four threads a
+// group of 32, so a group's minimum and maximum are two shuffles, every load
+// and store of values is 16 bytes or more per thread, and no two tokens share
+// a stored byte (no read-modify-write between threads).  The floor is the
+// bytes of both sides; what bounds the kernels are instructions, so the place
+// in the cache is found once for key and value and in 32 bits, and the
+// quantiser keeps off the conversion and 64-bit units.
 #include "kv4.cuh"
 
 namespace redlite {
@@ -26,6 +28,23 @@ struct Kv4Args {
   int32_t *status;
 };
 
+// A block's rows: row i of `kRows` is head i % n_heads of token blockIdx.x *
+// tokens + i / n_heads; more heads than rows continue in blockIdx.y.
+template <int D>
+struct Rows {
+  static constexpr int kWords = D / 8, kRows = 256 / kWords;
+  int64_t token;
+  int head;
+  bool live;
+  __device__ __forceinline__ explicit Rows(const Kv4Args &a) {
+    const unsigned i = threadIdx.x / kWords, heads = a.n_heads, tokens = heads < kRows ? kRows / heads : 1u;
+    const unsigned t = heads < kRows ? i / heads : 0u;
+    head = (int)(heads < kRows ? i - t * heads : blockIdx.y * kRows + i);
+    token = (int64_t)blockIdx.x * tokens + t;
+    live = t < tokens && head < a.n_heads && token < a.n_tokens;
+  }
+};
+
 // Where a row's tile lies, or null (a row behind the last sequence, or a page
 // the table does not name: reported).
 template <int D>
@@ -33,131 +52,141 @@ __device__ __forceinline__ uint8_t *row_tile(const Kv4Args &a, int64_t row, int 
   const int s = find_seq(a.cu, a.n_seqs, row);
   skip = s < 0;
   if (skip) return nullptr;
-  const int64_t pos = (int64_t)__ldg(a.start + s) + (row - __ldg(a.cu + s));
-  if (pos < 0 || pos / a.page_size >= a.max_pages) {
+  const int64_t at = (int64_t)__ldg(a.start + s) + (row - __ldg(a.cu + s));
+  const uint32_t pos = (uint32_t)at, p = pos / (uint32_t)a.page_size;  // a sum of two numbers below 2^31
+  if (at < 0 || p >= (uint32_t)a.max_pages) {
     set_status(a.status, REDLITE_STATUS_BAD_LENGTH);
     return nullptr;
   }
-  const int64_t page = __ldg(a.table + (int64_t)s * a.max_pages + pos / a.page_size);
+  const int64_t page = __ldg(a.table + (int64_t)s * a.max_pages + p);
   if (page < 0 || page >= a.n_pages) {
     set_status(a.status, REDLITE_STATUS_BAD_PAGE);
     return nullptr;
   }
-  const int in_page = (int)(pos % a.page_size);
+  const int in_page = (int)(pos - p * (uint32_t)a.page_size);
   tok = in_page & 15;
   return a.cache + kv4_tile_offset<D>(page, a.n_heads, head, a.page_size, in_page >> 4);
 }
 
-// Threads of one value row (key or value of one token and head).
-template <typename T, int D>
-__global__ void __launch_bounds__(256) kv4_append_kernel(Kv4Args a) {
-  constexpr int kWords = D / 8;
-  const int64_t id = (int64_t)blockIdx.x * (256 / kWords) + threadIdx.x / kWords;
-  const int w = threadIdx.x % kWords;
-  const int64_t n = (int64_t)a.n_tokens * a.n_heads * 2;
-  // a row's threads share these conditions, and the shuffles below stay
-  // inside groups of four threads of one row
-  const bool live = id < n;
-  const bool is_v = id & 1;
-  const int64_t row = (id >> 1) / a.n_heads;
-  const int head = (int)((id >> 1) % a.n_heads);
-  int tok = 0;
-  bool skip = true;
-  uint8_t *tile = live ? row_tile<D>(a, row, head, tok, skip) : nullptr;
-  float x[8];
-  if (tile) {
-    const T *src = (is_v ? (const T *)a.v + row * a.v_stride : (const T *)a.k + row * a.k_stride) + head * D + w * 8;
-    load8<T>(src, x);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = 0.f;
-  }
-  bool finite = true;
+// Codes of eight values and the step and minimum of their group of 32 (four
+// threads).  Step and minimum are stored in 16 bits (11 significant ones, a
+// quarter of a bit per value); the codes are chosen for the stored pair.
+__device__ __forceinline__ uint32_t quantise(const float (&x)[8], __half &dh, __half &mh) {
+  float odd = 0.f;  // a NaN once a value is not finite
   float lo = INFINITY, hi = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    finite = finite && isfinite(x[i]);
-    x[i] = fminf(fmaxf(x[i], -65504.f), 65504.f);
-    lo = fminf(lo, x[i]), hi = fmaxf(hi, x[i]);
-  }
+  for (int i = 0; i < 8; ++i) odd = fmaf(x[i], 0.f, odd), lo = fminf(lo, x[i]), hi = fmaxf(hi, x[i]);
 #pragma unroll
   for (int o = 1; o <= 2; o <<= 1) {
     lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
     hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-    finite = __shfl_xor_sync(0xffffffffu, (int)finite, o) && finite;
+    odd += __shfl_xor_sync(0xffffffffu, odd, o);
   }
-  // step and minimum are stored in 16 bits (11 significant ones, a quarter of
-  // a bit per value); the codes are chosen for the stored pair, with the
-  // quotient in 64 bits so that a value next to the border between two codes
-  // gets the nearer one
-  __half mh = __float2half_rn(lo);
+  // a value outside +-65504 gets the code of the end it lies behind
+  lo = fminf(fmaxf(lo, -65504.f), 65504.f), hi = fminf(fmaxf(hi, -65504.f), 65504.f);
+  mh = __float2half_rn(lo);
   const float m = __half2float(mh);
-  __half dh = __float2half_rn(__fdiv_rn(__fsub_rn(hi, m), 15.f));
-  const double d = (double)__half2float(dh);
+  dh = __float2half_rn(__fdiv_rn(__fsub_rn(hi, m), 15.f));
+  const float d = __half2float(dh);
   uint32_t word = 0;
-  if (d > 0.0 && finite) {
+  if (odd != 0.f) {  // a group that holds a NaN or an infinity reads back as NaN
+    mh = dh = __ushort_as_half(0x7fff);
+  } else if (d > 0.f) {
+    // The quotient in fp32 is off by 15 x 2^-21 at most; the sum with 1.5 x
+    // 2^23 rounds it to a whole number (ties to even) in its low bits.  One
+    // within 2^-16 of the border between two codes is decided in 64 bits, by
+    // the side of the border that the value lies on (16-bit inputs meet the
+    // border itself once in a thousand).
+    const float inv = __fdividef(1.f, d);
+    uint32_t near = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const double c = rint(((double)x[i] - (double)m) / d);
-      word |= (uint32_t)fmin(fmax(c, 0.0), 15.0) << (4 * i);
+      const float y = fminf(fmaxf(__fsub_rn(x[i], m) * inv, 0.f), 15.f), z = y + 12582912.f;
+      if (fabsf(y - (z - 12582912.f)) > 0.5f - 0x1p-16f) near |= 1u << (4 * i);
+      word += (__float_as_uint(z) & 15u) << (4 * i);
+    }
+    while (near) {
+      const int at = __ffs(near) - 1;
+      near &= near - 1;
+      float v = x[0];
+#pragma unroll
+      for (int j = 1; j < 8; ++j) v = at == 4 * j ? x[j] : v;
+      const float below = floorf(__fsub_rn(v, m) * inv);
+      const double side = fma(-((double)below + 0.5), (double)d, (double)v - (double)m);
+      const uint32_t k = (uint32_t)below, code = side > 0.0 || (side == 0.0 && (k & 1u)) ? k + 1 : k;
+      word = (word & ~(15u << at)) | (code << at);
     }
   }
-  if (!finite) {  // a group that holds a NaN or an infinity reads back as NaN
-    mh = __ushort_as_half(0x7fff);
-    dh = mh;
-  }
-  if (!tile) return;
-  const int g = w >> 2, c = w & 3;
-  if (!is_v) {
-    *reinterpret_cast<uint32_t *>(tile + kv4_k_word<D>(tok, g, c)) = word;
-    if (c == 0) *reinterpret_cast<__half2 *>(tile + kv4_k_step<D>(tok, g)) = __halves2half2(dh, mh);
-  } else {
-    *reinterpret_cast<uint16_t *>(tile + kv4_v_unit<D>(tok, g, 2 * c)) = (uint16_t)word;
-    *reinterpret_cast<uint16_t *>(tile + kv4_v_unit<D>(tok, g, 2 * c + 1)) = (uint16_t)(word >> 16);
-    if (c == 0) {
-      *reinterpret_cast<__half *>(tile + kv4_v_step<D>(tok, g)) = dh;
-      *reinterpret_cast<__half *>(tile + kv4_v_min<D>(tok, g)) = mh;
-    }
-  }
+  return word;
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(256) kv4_load_kernel(Kv4Args a) {
-  constexpr int kWords = D / 8;
-  const int64_t id = (int64_t)blockIdx.x * (256 / kWords) + threadIdx.x / kWords;
-  const int w = threadIdx.x % kWords;
-  if (id >= (int64_t)a.n_tokens * a.n_heads * 2) return;
-  const bool is_v = id & 1;
-  const int64_t row = (id >> 1) / a.n_heads;
-  const int head = (int)((id >> 1) % a.n_heads);
+__global__ void __launch_bounds__(256) kv4_append_kernel(const Kv4Args a) {
+  const Rows<D> row(a);
+  const int w = threadIdx.x % Rows<D>::kWords, g = w >> 2, c = w & 3;
+  // a row's threads share these conditions, and the shuffles stay inside
+  // groups of four threads of one row
+  float x[8], y[8];
+  if (row.live) {
+    load8<T>((const T *)a.k + row.token * a.k_stride + row.head * D + w * 8, x);
+    load8<T>((const T *)a.v + row.token * a.v_stride + row.head * D + w * 8, y);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = y[i] = 0.f;
+  }
+  int tok = 0;
+  bool skip = true;
+  uint8_t *tile = row.live ? row_tile<D>(a, row.token, row.head, tok, skip) : nullptr;
+  __half dk, mk, dv, mv;
+  const uint32_t kw = quantise(x, dk, mk), vw = quantise(y, dv, mv);
+  if (!tile) return;
+  *reinterpret_cast<uint32_t *>(tile + kv4_k_word<D>(tok, g, c)) = kw;
+  uint16_t *vu = reinterpret_cast<uint16_t *>(tile + kv4_v_unit<D>(tok, g, 2 * c));
+  vu[0] = (uint16_t)vw, vu[32] = (uint16_t)(vw >> 16);  // the next eighth of the group lies 32 units on
+  if (c == 0) {
+    *reinterpret_cast<__half2 *>(tile + kv4_k_step<D>(tok, g)) = __halves2half2(dk, mk);
+    *reinterpret_cast<__half *>(tile + kv4_v_step<D>(tok, g)) = dv;
+    *reinterpret_cast<__half *>(tile + kv4_v_min<D>(tok, g)) = mv;
+  }
+}
+
+// d * code is exact; the code as the low bits of 2^23 + code.
+__device__ __forceinline__ void expand(uint32_t word, float d, float m, float (&x)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = fmaf(d, __uint_as_float(((word >> (4 * i)) & 15u) | 0x4b000000u) - 8388608.f, m);
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(256) kv4_load_kernel(const Kv4Args a) {
+  const Rows<D> row(a);
+  if (!row.live) return;
+  const int w = threadIdx.x % Rows<D>::kWords, g = w >> 2, c = w & 3;
   int tok = 0;
   bool skip = false;
-  const uint8_t *tile = row_tile<D>(a, row, head, tok, skip);
+  const uint8_t *tile = row_tile<D>(a, row.token, row.head, tok, skip);
   if (skip) return;
-  const int g = w >> 2, c = w & 3;
-  uint32_t word = 0;
-  float d = 0.f, m = 0.f;  // a position without a page reads as zeros (reported)
-  if (tile && !is_v) {
-    word = *reinterpret_cast<const uint32_t *>(tile + kv4_k_word<D>(tok, g, c));
+  uint32_t kw = 0, vw = 0;
+  float dk = 0.f, mk = 0.f, dv = 0.f, mv = 0.f;  // a position without a page reads as zeros (reported)
+  if (tile) {
+    kw = *reinterpret_cast<const uint32_t *>(tile + kv4_k_word<D>(tok, g, c));
+    const uint16_t *vu = reinterpret_cast<const uint16_t *>(tile + kv4_v_unit<D>(tok, g, 2 * c));
+    vw = vu[0] | ((uint32_t)vu[32] << 16);
     const __half2 dm = *reinterpret_cast<const __half2 *>(tile + kv4_k_step<D>(tok, g));
-    d = __low2float(dm), m = __high2float(dm);
-  } else if (tile) {
-    word = *reinterpret_cast<const uint16_t *>(tile + kv4_v_unit<D>(tok, g, 2 * c)) |
-           ((uint32_t)*reinterpret_cast<const uint16_t *>(tile + kv4_v_unit<D>(tok, g, 2 * c + 1)) << 16);
-    d = __half2float(*reinterpret_cast<const __half *>(tile + kv4_v_step<D>(tok, g)));
-    m = __half2float(*reinterpret_cast<const __half *>(tile + kv4_v_min<D>(tok, g)));
+    dk = __low2float(dm), mk = __high2float(dm);
+    dv = __half2float(*reinterpret_cast<const __half *>(tile + kv4_v_step<D>(tok, g)));
+    mv = __half2float(*reinterpret_cast<const __half *>(tile + kv4_v_min<D>(tok, g)));
   }
   float x[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = fmaf(d, (float)((word >> (4 * i)) & 15u), m);  // d * code is exact
-  T *dst = (is_v ? (T *)a.vo + row * a.v_stride : (T *)a.ko + row * a.k_stride) + head * D + w * 8;
-  store8<T>(dst, x);
+  expand(kw, dk, mk, x);
+  store8<T>((T *)a.ko + row.token * a.k_stride + row.head * D + w * 8, x);
+  expand(vw, dv, mv, x);
+  store8<T>((T *)a.vo + row.token * a.v_stride + row.head * D + w * 8, x);
 }
 
 template <bool APPEND, typename T>
 cudaError_t launch_rows(const Kv4Args &a, int D, cudaStream_t s) {
-  const int64_t rows = (int64_t)a.n_tokens * a.n_heads * 2, per = 256 / (D / 8);
-  const unsigned grid = (unsigned)((rows + per - 1) / per);
+  const int64_t per = a.n_heads, rows = 256 / (D / 8), tokens = per < rows ? rows / per : 1;
+  const dim3 grid((unsigned)((a.n_tokens + tokens - 1) / tokens), (unsigned)((per + rows - 1) / rows));
   if (D == 256) {
     if (APPEND) kv4_append_kernel<T, 256><<<grid, 256, 0, s>>>(a);
     else kv4_load_kernel<T, 256><<<grid, 256, 0, s>>>(a);
@@ -180,7 +209,6 @@ int run_rows(int32_t dtype, const void *k, const void *v, int64_t k_stride, int6
   if (!aligned16(k) || !aligned16(v) || !aligned16(cache)) return REDLITE_EINVAL;
   const int64_t row = (int64_t)n_kv_heads * head_dim;
   if (!stride_ok(k_stride, row, dtype) || !stride_ok(v_stride, row, dtype)) return REDLITE_EINVAL;
-  if ((int64_t)n_tokens * n_kv_heads * 2 * (head_dim / 8) / 256 >= ((int64_t)1 << 31) - 1) return REDLITE_EUNSUPPORTED;
   Kv4Args a;
   a.k = k, a.v = v, a.ko = const_cast<void *>(k), a.vo = const_cast<void *>(v);
   a.k_stride = k_stride, a.v_stride = v_stride;
