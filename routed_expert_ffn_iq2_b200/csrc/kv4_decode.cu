@@ -9,16 +9,18 @@
 // The floor is the cache's bytes (1.25 D per token and key/value head, both
 // sides), each read once; what stands beside it is the conversion of the
 // codes, so the kernel never forms the values.  Codes go to the tensor cores
-// as the exact bf16 numbers 1 + code / 16 (one shift and one and-or for two of
-// them), with
+// as exact small numbers (a shift, an and-or for two of them):
 //   q . K_t   = sum_g 16 d_tg (q_g . (1 + code / 16)) + (m_tg - 16 d_tg) sum(q_g)
-//   o of g    = sum_t (16 d_tg p_t) (code - 8) / 16 + sum_t p_t (m_tg + 8 d_tg):
-// steps and minima are applied in fp32 to the 16 x 8 products (keys) and to
-// the 16 probabilities (values), once per group of 32 values.  Queries are
-// split into bf16 parts that hold them exactly (1 part for bf16, 2 for fp16,
-// 3 for fp32); 16 d p and p are split into two parts (what is left out is at
-// most 2^-17 of each product).  Sums, maxima and the running softmax
-// statistics are fp32.
+//   o of g    = sum_t (p_t d_tg) (code - 8) + sum_t p_t (m_tg + 8 d_tg)
+// with the sums over m and d as products of their own (their stored fp16
+// numbers are operands as they lie).  Two forms of the rest:
+//   16-bit activations  a head's query scaled by a power of two into one fp16
+//               part (exact); p d is one fp16 product (2^-11 of each term at
+//               most, below what the outputs' type rounds).  The reference of
+//               the softmax is kept so that neither p nor p d leaves fp16:
+//               p <= 2^15 / max(1, |d|) for the largest |d| met so far.
+//   fp32        the query in three bf16 parts (exact); 16 d p and p in three.
+// Sums, maxima and the running softmax statistics are fp32.
 //
 // Split: the units of all sequences (128 tokens of one key/value head and up
 // to 8 of its query heads) form one list, cut evenly over a fixed grid; a
@@ -34,6 +36,7 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kUnit = 16 * kWarps;  // tokens of a unit
 constexpr float kLazy = 8.f;        // log2 by which scores may pass the reference before sums are rescaled
+constexpr float kTop = 15.f;        // log2 that p, and p |d|, stay below in fp16
 
 struct DecArgs {
   const void *q;
@@ -99,17 +102,7 @@ __device__ __forceinline__ int64_t scan_units(const DecArgs &a, int64_t *sm) {
 }
 
 template <typename T>
-struct Splits {
-  static constexpr int n = 1;
-};
-template <>
-struct Splits<__half> {
-  static constexpr int n = 2;
-};
-template <>
-struct Splits<float> {
-  static constexpr int n = 3;
-};
+constexpr int kParts = sizeof(T) == 2 ? 1 : 3;  // parts of a query
 
 template <int D>
 struct DecSmem {
@@ -121,12 +114,17 @@ struct DecSmem {
 
 template <typename T, int D>
 constexpr int dec_smem_bytes() {
-  return DecSmem<D>::kRing + Splits<T>::n * (D / 32) * 512 + (D / 32) * 32 + kWarps * 8 * 8 +
+  return DecSmem<D>::kRing + kParts<T> * (D / 32) * 512 + (D / 32) * 32 + 8 * 4 + kWarps * 8 * 8 +
          kWarps * DecSmem<D>::kStages * 8 + (4 + kWarps) * 8 + 32;
 }
 
-// (1 + code / 16) as bf16 pairs from nibble i of both halves of w.
+// (1 + code / 16) pairs from nibble i of both halves of w: bf16 or fp16.
+template <bool F16>
 __device__ __forceinline__ uint32_t code_pair(uint32_t w, int i) {
+  if (F16) {
+    const uint32_t x = i == 0 ? w << 6 : (i == 1 ? w << 2 : (i == 2 ? w >> 2 : w >> 6));
+    return (x & 0x03c003c0u) | 0x3c003c00u;
+  }
   const uint32_t x = i == 0 ? w << 3 : w >> (4 * i - 3);
   return (x & 0x00780078u) | 0x3f803f80u;
 }
@@ -136,18 +134,42 @@ __device__ __forceinline__ uint32_t centre(uint32_t v) {
   asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(0x3fc03fc0u));
   return r;
 }
+__device__ __forceinline__ __half2 as_h2(uint32_t v) { return *reinterpret_cast<const __half2 *>(&v); }
+__device__ __forceinline__ uint32_t as_u32(__half2 v) { return *reinterpret_cast<const uint32_t *>(&v); }
+// The four (code - 8) pairs of w in fp16, exact: 1024 + code (or 1024 + 16
+// code, from the second nibble where it stands) less what is too much.
+__device__ __forceinline__ void codes_centred(uint32_t w, uint32_t (&v)[4]) {
+  const __half2 k = __half2half2(__float2half(-1032.f)), f = __half2half2(__float2half(0.0625f)),
+                t = __half2half2(__float2half(-72.f));
+  const uint32_t x = w >> 8;
+  v[0] = as_u32(__hadd2(as_h2((w & 0x000f000fu) | 0x64006400u), k));
+  v[1] = as_u32(__hfma2(as_h2((w & 0x00f000f0u) | 0x64006400u), f, t));
+  v[2] = as_u32(__hadd2(as_h2((x & 0x000f000fu) | 0x64006400u), k));
+  v[3] = as_u32(__hfma2(as_h2((x & 0x00f000f0u) | 0x64006400u), f, t));
+}
+__device__ __forceinline__ void mma_f16_k8(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(b));
+}
+__device__ __forceinline__ void ldsm2(uint32_t addr, uint32_t &a, uint32_t &b) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0,%1}, [%2];" : "=r"(a), "=r"(b) : "r"(addr) : "memory");
+}
 __device__ __forceinline__ float h_lo(uint32_t v) { return __half2float(__ushort_as_half((uint16_t)v)); }
 __device__ __forceinline__ float h_hi(uint32_t v) { return __half2float(__ushort_as_half((uint16_t)(v >> 16))); }
 
 template <typename T, int D>
 __global__ void __launch_bounds__(32 * kWarps, 2) kv4_decode_kernel(const DecArgs a) {
   using S = DecSmem<D>;
-  constexpr int NG = S::NG, NS = Splits<T>::n, kStages = S::kStages;
+  constexpr int NG = S::NG, NS = kParts<T>, kStages = S::kStages;
+  constexpr bool kHalf = sizeof(T) == 2;
   extern __shared__ __align__(128) uint8_t smem[];
   uint8_t *ring_all = smem;
   uint4 *qf = reinterpret_cast<uint4 *>(smem + S::kRing);             // [NS][NG][32]
   float *qs = reinterpret_cast<float *>(qf + NS * NG * 32);          // [NG][8]
-  float2 *ml = reinterpret_cast<float2 *>(qs + NG * 8);              // [kWarps][8] {m, l}
+  float *qinv = qs + NG * 8;                                         // [8] inverse scale of a head's query
+  float2 *ml = reinterpret_cast<float2 *>(qinv + 8);                 // [kWarps][8] {m, l}
   uint64_t *bars = reinterpret_cast<uint64_t *>(ml + kWarps * 8);    // [kWarps][kStages]
   int64_t *scan = reinterpret_cast<int64_t *>(bars + kWarps * kStages);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, c = lane & 3;
@@ -199,63 +221,109 @@ __global__ void __launch_bounds__(32 * kWarps, 2) kv4_decode_kernel(const DecArg
     const int n_it = tile0 < tile_end ? (tile_end - tile0 + kWarps - 1) / kWarps : 0;
     const int tiles_per_page = a.page_size >> 4;
     const int32_t *table = a.table + (int64_t)seq * a.max_pages;
-    // lane i holds the page of tile number `batch + i`
+    // lane i holds the place of tile number `batch + i`, or -1
     int batch = -32;
-    int64_t my_page = -1;
+    int64_t my_at = -1;
     auto issue = [&](int it) {
       if (it - batch >= 32) {
         batch = it;
-        const int t = tile0 + kWarps * (it + lane);
-        my_page = it + lane < n_it ? (int64_t)__ldg(table + t / tiles_per_page) : -1;
-        if (it + lane < n_it && (my_page < 0 || my_page >= a.n_pages)) {
-          set_status(a.status, REDLITE_STATUS_BAD_PAGE);
-          my_page = -1;
+        my_at = -1;
+        if (it + lane < n_it) {
+          const unsigned t = tile0 + kWarps * (it + lane), p = t / (unsigned)tiles_per_page;
+          const int64_t page = __ldg(table + p);
+          if (page < 0 || page >= a.n_pages)
+            set_status(a.status, REDLITE_STATUS_BAD_PAGE);
+          else
+            my_at = kv4_tile_offset<D>(page, a.n_kv, kvh, a.page_size, (int)(t - p * tiles_per_page));
         }
       }
-      const int64_t page = __shfl_sync(0xffffffffu, my_page, it - batch);
+      const int64_t at = __shfl_sync(0xffffffffu, my_at, it - batch);
       if (lane == 0) {
-        const int st = it % kStages, t = tile0 + kWarps * it;
-        if (page >= 0) {
+        const int st = it % kStages;
+        if (at >= 0) {
           ptx::mbar_expect_tx(bar + st, S::kTile);
-          ptx::bulk_g2s(ring + st * S::kTile,
-                        a.cache + kv4_tile_offset<D>(page, a.n_kv, kvh, a.page_size, t % tiles_per_page), S::kTile,
-                        bar + st);
+          ptx::bulk_g2s(ring + st * S::kTile, a.cache + at, S::kTile, bar + st);
         } else {
           ptx::mbar_arrive(bar + st);  // nothing is read: the tile is masked below
         }
       }
-      return page >= 0;
+      return at >= 0;
     };
     uint32_t good = 0;  // bit i: the tile in stage i is real
 #pragma unroll
     for (int i = 0; i < kStages; ++i)
       if (i < n_it) good |= (uint32_t)issue(i) << i;
 
-    // ---- queries of the block's heads as bf16 parts, and their sums per group
-    for (int i = tid; i < NG * 32; i += 32 * kWarps) {
-      const int g = i >> 5, rr = (i >> 2) & 7, cc = i & 3;
-      float x[8];
+    // ---- queries of the block's heads as parts, and their sums per group
+    auto query = [&](int g, int rr, int cc, float (&x)[8]) {
       if (rr < n_h) {
         load8<T>((const T *)a.q + (int64_t)seq * a.q_stride + (int64_t)(head0 + rr) * D + 32 * g + 8 * cc, x);
       } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] = 0.f;
       }
-      float sum = ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
-      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      if (cc == 0) qs[g * 8 + rr] = sum;
+    };
+    if (kHalf) {
+      // a warp per head; its largest element goes to 2^9, so that a group's sum stays below 2^14
+      const int rr = warp;
+      float y[NG / 4][8], mx = 0.f;
 #pragma unroll
-      for (int p = 0; p < NS; ++p) {
-        uint4 w;  // pairs (0,4) (1,5) (2,6) (3,7): nibble i of both halves of a code word
-        w.x = pack_bf16(x[0], x[4]), w.y = pack_bf16(x[1], x[5]);
-        w.z = pack_bf16(x[2], x[6]), w.w = pack_bf16(x[3], x[7]);
-        qf[(p * NG + g) * 32 + (i & 31)] = w;
-        x[0] -= bf16_lo(w.x), x[4] -= bf16_hi(w.x), x[1] -= bf16_lo(w.y), x[5] -= bf16_hi(w.y);
-        x[2] -= bf16_lo(w.z), x[6] -= bf16_hi(w.z), x[3] -= bf16_lo(w.w), x[7] -= bf16_hi(w.w);
+      for (int i = 0; i < NG / 4; ++i) {
+        query(4 * i + (lane >> 3), rr, (lane >> 1) & 3, y[i]);  // two lanes per piece
+#pragma unroll
+        for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(y[i][e]));
+      }
+#pragma unroll
+      for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      float inv;
+      const float s = scale_f16(mx, inv) * 0x1p-5f;
+      if (lane == 0) qinv[rr] = inv * 0x1p5f;
+#pragma unroll
+      for (int i = 0; i < NG / 4; ++i) {
+        const int g = 4 * i + (lane >> 3), cc = (lane >> 1) & 3;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[i][e] *= s;
+        float sum = ((y[i][0] + y[i][1]) + (y[i][2] + y[i][3])) + ((y[i][4] + y[i][5]) + (y[i][6] + y[i][7]));
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+        if ((lane & 7) == 0) qs[g * 8 + rr] = sum;
+        if ((lane & 1) == 0)  // pairs (0,4) (1,5) (2,6) (3,7): nibble i of both halves of a code word
+          qf[g * 32 + rr * 4 + cc] = make_uint4(pack_f16(y[i][0], y[i][4]), pack_f16(y[i][1], y[i][5]),
+                                                pack_f16(y[i][2], y[i][6]), pack_f16(y[i][3], y[i][7]));
+      }
+    } else {
+      for (int i = tid; i < NG * 32; i += 32 * kWarps) {
+        const int g = i >> 5, rr = (i >> 2) & 7, cc = i & 3;
+        float x[8];
+        query(g, rr, cc, x);
+        float sum = ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        if (cc == 0) qs[g * 8 + rr] = sum;
+#pragma unroll
+        for (int p = 0; p < NS; ++p) {
+          uint4 w;
+          w.x = pack_bf16(x[0], x[4]), w.y = pack_bf16(x[1], x[5]);
+          w.z = pack_bf16(x[2], x[6]), w.w = pack_bf16(x[3], x[7]);
+          qf[(p * NG + g) * 32 + (i & 31)] = w;
+          x[0] -= bf16_lo(w.x), x[4] -= bf16_hi(w.x), x[1] -= bf16_lo(w.y), x[5] -= bf16_hi(w.y);
+          x[2] -= bf16_lo(w.z), x[6] -= bf16_hi(w.z), x[3] -= bf16_lo(w.w), x[7] -= bf16_hi(w.w);
+        }
       }
     }
     __syncthreads();
+    // coefficients of {d, m} of groups c and c + 4 in a score of head r (in
+    // units of 16 d): fp16 parts
+    uint32_t ch[2] = {0u, 0u}, cl[2] = {0u, 0u};
+    float to_log2 = a.scale_log2;
+    if (kHalf) {
+      to_log2 *= 16.f * qinv[r];
+#pragma unroll
+      for (int i = 0; i < NG / 4; ++i) {
+        const float v = qs[(c + 4 * i) * 8 + r];
+        split_f16(-v, v * 0.0625f, ch[i], cl[i]);
+      }
+    }
 
     float acc[NG][2][4], accm[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -265,6 +333,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) kv4_decode_kernel(const DecArg
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[g][e][i] = 0.f;
     float m_run = -INFINITY, l_run = 0.f;  // of query head r; l over this thread's tokens
+    float room = kTop;  // log2 that p may reach: kTop less the largest log2 |d| met (16-bit types)
 
     for (int it = 0; it < n_it; ++it) {
       const int st = it % kStages;
@@ -276,6 +345,18 @@ __global__ void __launch_bounds__(32 * kWarps, 2) kv4_decode_kernel(const DecArg
       const int live = ((good >> st) & 1u) ? len - tok0 : 0;  // tokens of this tile that count
       // ---- scores: C[token][head] over the groups
       float s[4] = {0.f, 0.f, 0.f, 0.f};
+      if (kHalf) {  // the terms of d and m alone
+        uint32_t k[4];
+        if (NG == 8) {
+          ldsm4(tile + 8 * D + (lane & 15) * 32 + (lane >> 4) * 16, k[0], k[1], k[2], k[3]);
+          mma_f16(s, k, ch[0], ch[1]);
+          mma_f16(s, k, cl[0], cl[1]);
+        } else {
+          ldsm2(tile + 8 * D + (lane & 15) * 16, k[0], k[1]);
+          mma_f16_k8(s, k[0], k[1], ch[0]);
+          mma_f16_k8(s, k[0], k[1], cl[0]);
+        }
+      }
 #pragma unroll
       for (int gq = 0; gq < NG / 4; ++gq) {
         const uint4 w0 = ptx::lds128(tile + gq * 512 + lane * 16);               // token r
@@ -289,21 +370,31 @@ __global__ void __launch_bounds__(32 * kWarps, 2) kv4_decode_kernel(const DecArg
           const int g = gq * 4 + gg;
           uint32_t A0[4], A1[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) A0[i] = code_pair(wa[gg], i), A1[i] = code_pair(wb[gg], i);
+          for (int i = 0; i < 4; ++i) A0[i] = code_pair<kHalf>(wa[gg], i), A1[i] = code_pair<kHalf>(wb[gg], i);
           float x[4] = {0.f, 0.f, 0.f, 0.f};
+          if (kHalf) {
+            const uint4 b = qf[g * 32 + lane];
+            const uint32_t p[4] = {A0[0], A1[0], A0[1], A1[1]}, q[4] = {A0[2], A1[2], A0[3], A1[3]};
+            mma_f16(x, p, b.x, b.y);
+            mma_f16(x, q, b.z, b.w);
+            const float da = h_lo(ka[gg]), db = h_lo(kb[gg]);
+            s[0] = fmaf(da, x[0], s[0]), s[1] = fmaf(da, x[1], s[1]);
+            s[2] = fmaf(db, x[2], s[2]), s[3] = fmaf(db, x[3], s[3]);
+          } else {
 #pragma unroll
-          for (int p = 0; p < NS; ++p) {
-            const uint4 b = qf[(p * NG + g) * 32 + lane];
-            mma_bf16(x, A0[0], A1[0], A0[1], A1[1], b.x, b.y);
-            mma_bf16(x, A0[2], A1[2], A0[3], A1[3], b.z, b.w);
+            for (int p = 0; p < NS; ++p) {
+              const uint4 b = qf[(p * NG + g) * 32 + lane];
+              mma_bf16(x, A0[0], A1[0], A0[1], A1[1], b.x, b.y);
+              mma_bf16(x, A0[2], A1[2], A0[3], A1[3], b.z, b.w);
+            }
+            const float2 sum = *reinterpret_cast<const float2 *>(qs + g * 8 + 2 * c);
+            const float da = 16.f * h_lo(ka[gg]), db = 16.f * h_lo(kb[gg]);
+            const float ma = h_hi(ka[gg]) - da, mb = h_hi(kb[gg]) - db;
+            s[0] = fmaf(da, x[0], fmaf(ma, sum.x, s[0]));
+            s[1] = fmaf(da, x[1], fmaf(ma, sum.y, s[1]));
+            s[2] = fmaf(db, x[2], fmaf(mb, sum.x, s[2]));
+            s[3] = fmaf(db, x[3], fmaf(mb, sum.y, s[3]));
           }
-          const float2 sum = *reinterpret_cast<const float2 *>(qs + g * 8 + 2 * c);
-          const float da = 16.f * h_lo(ka[gg]), db = 16.f * h_lo(kb[gg]);
-          const float ma = h_hi(ka[gg]) - da, mb = h_hi(kb[gg]) - db;
-          s[0] = fmaf(da, x[0], fmaf(ma, sum.x, s[0]));
-          s[1] = fmaf(da, x[1], fmaf(ma, sum.y, s[1]));
-          s[2] = fmaf(db, x[2], fmaf(mb, sum.x, s[2]));
-          s[3] = fmaf(db, x[3], fmaf(mb, sum.y, s[3]));
         }
       }
       // ---- to the layout of the second product: head r, tokens 2c, 2c+1, 2c+8, 2c+9
@@ -317,15 +408,51 @@ __global__ void __launch_bounds__(32 * kWarps, 2) kv4_decode_kernel(const DecArg
         p[0] = (r & 1) ? a1 : a0, p[1] = (r & 1) ? b1 : b0;
         p[2] = (r & 1) ? c1 : c0, p[3] = (r & 1) ? d1 : d0;
       }
+      // ---- steps of the four tokens
+      const uint32_t vs = tile + 18 * D, vm = tile + 19 * D;
+      uint32_t dw[4][NG / 2];
+      int tk[4];
+      bool on[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) p[i] = 2 * c + (i & 1) + 8 * (i >> 1) < live ? p[i] * a.scale_log2 : -INFINITY;
+      for (int i = 0; i < 4; ++i) {
+        tk[i] = 2 * c + (i & 1) + 8 * (i >> 1), on[i] = tk[i] < live;
+        p[i] = on[i] ? p[i] * to_log2 : -INFINITY;
+        if (NG == 8) {
+          const uint4 d = ptx::lds128(vs + tk[i] * 16);
+          dw[i][0] = d.x, dw[i][1] = d.y, dw[i][NG / 2 - 2] = d.z, dw[i][NG / 2 - 1] = d.w;
+        } else {
+          const uint2 d = ptx::lds64(vs + tk[i] * 8);
+          dw[i][0] = d.x, dw[i][1] = d.y;
+        }
+      }
+      if (live < 16) {  // what lies behind the sequence may be anything
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int g = 0; g < NG / 2; ++g) dw[i][g] = on[i] ? dw[i][g] : 0u;
+      }
       float mx = fmaxf(fmaxf(p[0], p[1]), fmaxf(p[2], p[3]));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      // rescale only when a score passes the reference by 2^8 (or the first
-      // one comes): the sums stay far inside fp32 either way
-      if (__any_sync(0xffffffffu, mx > m_run + kLazy || (m_run == -INFINITY && mx > -INFINITY))) {
-        const float m_new = fmaxf(m_run, mx);
+      if (kHalf) {
+        __half2 big = __habs2(as_h2(dw[0][0]));
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int g = 0; g < NG / 2; ++g)
+            if (i + g > 0) big = __hmax2(big, __habs2(as_h2(dw[i][g])));
+        big = __hmax2(big, as_h2(__shfl_xor_sync(0xffffffffu, as_u32(big), 1)));
+        big = __hmax2(big, as_h2(__shfl_xor_sync(0xffffffffu, as_u32(big), 2)));
+        const float top = fmaxf(__low2float(big), __high2float(big));
+        // 2^n > top for n = exponent + 1; at most 16
+        if (top >= 1.f) room = fminf(room, kTop - (float)min(16, (int)(__float_as_uint(top) >> 23) - 126));
+      }
+      // rescale only when a score passes the reference by 2^8 (16-bit types: by
+      // what keeps p and p d in fp16) or the first one comes: the sums stay far
+      // inside fp32 either way
+      const float limit = kHalf ? room : kLazy;
+      if (__any_sync(0xffffffffu, mx > m_run + limit || (m_run == -INFINITY && mx > -INFINITY))) {
+        const float m_new = kHalf ? (mx > m_run + limit ? mx - (limit - kLazy) : m_run) : fmaxf(m_run, mx);
         const float f = m_run == -INFINITY ? 0.f : ex2(m_run - m_new);
         l_run *= f;
         m_run = m_new;
@@ -340,65 +467,105 @@ __global__ void __launch_bounds__(32 * kWarps, 2) kv4_decode_kernel(const DecArg
       const float ref = m_run == -INFINITY ? 0.f : m_run;
 #pragma unroll
       for (int i = 0; i < 4; ++i) p[i] = ex2(p[i] - ref), l_run += p[i];
-      // ---- values
-      const uint32_t vs = tile + 18 * D, vm = tile + 19 * D;
-      int tk[4];
-      bool on[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) tk[i] = 2 * c + (i & 1) + 8 * (i >> 1), on[i] = tk[i] < live;
-      uint32_t ph[2], pl[2];
-      split_bf16(p[0], p[1], ph[0], pl[0]);
-      split_bf16(p[2], p[3], ph[1], pl[1]);
-      {
-        // group r's m + 8 d of the four tokens (rows r: high part, rows r + 8: low part)
-        float mid[4];
+      // ---- values (the code unit of slot i is token tk[i])
+      uint32_t vw[4][NG / 2];
+      if (NG == 8) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int g = r & (NG - 1);
-          const float d = h_lo(ptx::lds16(vs + (tk[i] * NG + g) * 2)), m = h_lo(ptx::lds16(vm + (tk[i] * NG + g) * 2));
-          mid[i] = on[i] && r < NG ? fmaf(8.f, d, m) : 0.f;
-        }
-        uint32_t h0, l0, h1, l1;
-        split_bf16(mid[0], mid[1], h0, l0);
-        split_bf16(mid[2], mid[3], h1, l1);
-        mma_bf16(accm, h0, l0, h1, l1, ph[0], ph[1]);
-        mma_bf16(accm, h0, l0, h1, l1, pl[0], pl[1]);
-      }
-      uint32_t vw[4][NG / 2], dw[4][NG / 2];  // codes and steps of the four tokens
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        // the code unit of slot i = 2 h + b is token 2 c + b + 8 h, as tk[i]
-        if (NG == 8) {
-          const uint4 v = ptx::lds128(tile + 10 * D + i * 512 + lane * 16), d = ptx::lds128(vs + tk[i] * 16);
+          const uint4 v = ptx::lds128(tile + 10 * D + i * 512 + lane * 16);
           vw[i][0] = v.x, vw[i][1] = v.y, vw[i][NG / 2 - 2] = v.z, vw[i][NG / 2 - 1] = v.w;
-          dw[i][0] = d.x, dw[i][1] = d.y, dw[i][NG / 2 - 2] = d.z, dw[i][NG / 2 - 1] = d.w;
-        } else {
-          const uint2 v = ptx::lds64(tile + 10 * D + (i >> 1) * 512 + lane * 16 + (i & 1) * 8);
-          const uint2 d = ptx::lds64(vs + tk[i] * 8);
-          vw[i][0] = v.x, vw[i][1] = v.y, dw[i][0] = d.x, dw[i][1] = d.y;
         }
-        p[i] *= 16.f;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+          const uint4 v = ptx::lds128(tile + 10 * D + (i >> 1) * 512 + lane * 16);
+          vw[i][0] = v.x, vw[i][1] = v.y, vw[i + 1][0] = v.z, vw[i + 1][1] = v.w;
+        }
       }
-#pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        float pd[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float d = (g & 1) ? h_hi(dw[i][g >> 1]) : h_lo(dw[i][g >> 1]);
-          pd[i] = on[i] ? p[i] * d : 0.f;
+      if (kHalf) {
+        uint32_t ph[2], pl[2], k[4];
+        split_f16(p[0], p[1], ph[0], pl[0]);
+        split_f16(p[2], p[3], ph[1], pl[1]);
+        // sums over m and d: rows r and r + 8 are m and d of group r (NG = 8),
+        // rows r and r + 4 (NG = 4)
+        if (NG == 8) {
+          ldsm4t(((lane & 8) ? vs : vm) + ((lane & 7) + ((lane >> 4) << 3)) * 16, k[0], k[1], k[2], k[3]);
+        } else {
+          const uint32_t at = (r < 4 ? vm : vs) + 2 * (r & 3);
+          k[0] = ptx::lds16(at + tk[0] * 8) | (ptx::lds16(at + tk[1] * 8) << 16);
+          k[2] = ptx::lds16(at + tk[2] * 8) | (ptx::lds16(at + tk[3] * 8) << 16);
+          k[1] = k[3] = 0u;
         }
-        uint32_t bh0, bl0, bh1, bl1;
-        split_bf16(pd[0], pd[1], bh0, bl0);
-        split_bf16(pd[2], pd[3], bh1, bl1);
-        const uint32_t sel = (g & 1) ? 0x7632u : 0x5410u;
-        const uint32_t X = __byte_perm(vw[0][g >> 1], vw[1][g >> 1], sel);
-        const uint32_t Y = __byte_perm(vw[2][g >> 1], vw[3][g >> 1], sel);
+        if (live < 16) {
+          const uint32_t m0 = (on[0] ? 0xffffu : 0u) | (on[1] ? 0xffff0000u : 0u);
+          const uint32_t m1 = (on[2] ? 0xffffu : 0u) | (on[3] ? 0xffff0000u : 0u);
+          k[0] &= m0, k[1] &= m0, k[2] &= m1, k[3] &= m1;
+        }
+        mma_f16(accm, k, ph[0], ph[1]);
+        mma_f16(accm, k, pl[0], pl[1]);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const uint32_t a0 = centre(code_pair(X, 2 * e)), a1 = centre(code_pair(X, 2 * e + 1));
-          const uint32_t a2 = centre(code_pair(Y, 2 * e)), a3 = centre(code_pair(Y, 2 * e + 1));
-          mma_bf16(acc[g][e], a0, a1, a2, a3, bh0, bh1);
-          mma_bf16(acc[g][e], a0, a1, a2, a3, bl0, bl1);
+        for (int g = 0; g < NG; ++g) {
+          const uint32_t sel = (g & 1) ? 0x7632u : 0x5410u;
+          const uint32_t b0 = as_u32(__hmul2(as_h2(ph[0]), as_h2(__byte_perm(dw[0][g >> 1], dw[1][g >> 1], sel))));
+          const uint32_t b1 = as_u32(__hmul2(as_h2(ph[1]), as_h2(__byte_perm(dw[2][g >> 1], dw[3][g >> 1], sel))));
+          uint32_t X[4], Y[4];
+          codes_centred(__byte_perm(vw[0][g >> 1], vw[1][g >> 1], sel), X);
+          codes_centred(__byte_perm(vw[2][g >> 1], vw[3][g >> 1], sel), Y);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint32_t A[4] = {X[2 * e], X[2 * e + 1], Y[2 * e], Y[2 * e + 1]};
+            mma_f16(acc[g][e], A, b0, b1);
+          }
+        }
+      } else {
+        // three parts of p, of 16 d p and of m + 8 d
+        auto parts = [](float x, float y, uint32_t (&w)[3]) {
+#pragma unroll
+          for (int i = 0; i < 3; ++i) {
+            w[i] = pack_bf16(x, y);
+            x -= bf16_lo(w[i]), y -= bf16_hi(w[i]);
+          }
+        };
+        uint32_t pa[3], pb[3];
+        parts(p[0], p[1], pa);
+        parts(p[2], p[3], pb);
+        {
+          // group r's m + 8 d of the four tokens (rows r: first part, rows r + 8:
+          // second; then the third alone)
+          float mid[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int g = r & (NG - 1);
+            const float d = h_lo(ptx::lds16(vs + (tk[i] * NG + g) * 2)), m = h_lo(ptx::lds16(vm + (tk[i] * NG + g) * 2));
+            mid[i] = on[i] && r < NG ? fmaf(8.f, d, m) : 0.f;
+          }
+          uint32_t ma[3], mb[3];
+          parts(mid[0], mid[1], ma);
+          parts(mid[2], mid[3], mb);
+#pragma unroll
+          for (int i = 0; i < 3; ++i) mma_bf16(accm, ma[0], ma[1], mb[0], mb[1], pa[i], pb[i]);
+          mma_bf16(accm, ma[2], 0u, mb[2], 0u, pa[0], pb[0]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[i] *= 16.f;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          float pd[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) pd[i] = p[i] * ((g & 1) ? h_hi(dw[i][g >> 1]) : h_lo(dw[i][g >> 1]));
+          uint32_t ba[3], bb[3];
+          parts(pd[0], pd[1], ba);
+          parts(pd[2], pd[3], bb);
+          const uint32_t sel = (g & 1) ? 0x7632u : 0x5410u;
+          const uint32_t X = __byte_perm(vw[0][g >> 1], vw[1][g >> 1], sel);
+          const uint32_t Y = __byte_perm(vw[2][g >> 1], vw[3][g >> 1], sel);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint32_t a0 = centre(code_pair<false>(X, 2 * e)), a1 = centre(code_pair<false>(X, 2 * e + 1));
+            const uint32_t a2 = centre(code_pair<false>(Y, 2 * e)), a3 = centre(code_pair<false>(Y, 2 * e + 1));
+#pragma unroll
+            for (int i = 0; i < 3; ++i) mma_bf16(acc[g][e], a0, a1, a2, a3, ba[i], bb[i]);
+          }
         }
       }
       // ---- the stage is free again
@@ -416,11 +583,17 @@ __global__ void __launch_bounds__(32 * kWarps, 2) kv4_decode_kernel(const DecArg
     if (c == 0) ml[warp * 8 + r] = make_float2(m_run, l_run);
     __syncwarp();
     float *mine = reinterpret_cast<float *>(ring);  // [8 heads][D]
-    accm[0] += accm[2], accm[1] += accm[3];  // high and low parts
+    // fp32: parts of the same sum; 16-bit types: rows of m, rows of d
+    const float of_d = kHalf ? 8.f : 1.f;
+    if (!kHalf || NG == 8) accm[0] = fmaf(of_d, accm[2], accm[0]), accm[1] = fmaf(of_d, accm[3], accm[1]);
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-      // group g's sum over m + 8 d sits in the lanes of row g
-      const float g0 = __shfl_sync(0xffffffffu, accm[0], g * 4 + c), g1 = __shfl_sync(0xffffffffu, accm[1], g * 4 + c);
+      // group g's sum over m + 8 d sits in the lanes of row g (and of row g + 4: d, where NG = 4)
+      float g0 = __shfl_sync(0xffffffffu, accm[0], g * 4 + c), g1 = __shfl_sync(0xffffffffu, accm[1], g * 4 + c);
+      if (kHalf && NG == 4) {
+        g0 = fmaf(8.f, __shfl_sync(0xffffffffu, accm[0], (g + 4) * 4 + c), g0);
+        g1 = fmaf(8.f, __shfl_sync(0xffffffffu, accm[1], (g + 4) * 4 + c), g1);
+      }
       float *h0 = mine + (2 * c) * D + 32 * g + 4 * r, *h1 = h0 + D;
       *reinterpret_cast<float4 *>(h0) =
           make_float4(acc[g][0][0] + g0, acc[g][0][2] + g0, acc[g][1][0] + g0, acc[g][1][2] + g0);
