@@ -9,11 +9,13 @@
 // The floor is the cache's bytes (1.25 D per token and key/value head, both
 // sides), each read once; what stands beside it is the conversion of the
 // codes, so the kernel never forms the values.  Codes go to the tensor cores
-// as exact small numbers (a shift, an and-or for two of them):
+// as exact small numbers (a shift, an and-or for two of them or more):
 //   q . K_t   = sum_g 16 d_tg (q_g . (1 + code / 16)) + (m_tg - 16 d_tg) sum(q_g)
 //   o of g    = sum_t (p_t d_tg) (code - 8) + sum_t p_t (m_tg + 8 d_tg)
 // with the sums over m and d as products of their own (their stored fp16
-// numbers are operands as they lie).  Two forms of the rest:
+// numbers are operands as they lie).  Where a code stands as 1 + code / 256
+// (that needs no shift of its own), the query's element is 16 times as large.
+// Two forms of the rest:
 //   16-bit activations  a head's query scaled by a power of two into one fp16
 //               part (exact); p d is one fp16 product (2^-11 of each term at
 //               most, below what the outputs' type rounds).  The reference of
@@ -114,19 +116,21 @@ struct DecSmem {
 
 template <typename T, int D>
 constexpr int dec_smem_bytes() {
-  return DecSmem<D>::kRing + kParts<T> * (D / 32) * 512 + (D / 32) * 32 + 8 * 4 + kWarps * 8 * 8 +
+  return DecSmem<D>::kRing + kParts<T> * (D / 32) * 512 + 2 * (D / 32) * 32 + 8 * 4 + kWarps * 8 * 8 +
          kWarps * DecSmem<D>::kStages * 8 + (4 + kWarps) * 8 + 32;
 }
 
-// (1 + code / 16) pairs from nibble i of both halves of w: bf16 or fp16.
-template <bool F16>
+// (1 + code / 16) pairs from nibble i of both halves of w, bf16.
 __device__ __forceinline__ uint32_t code_pair(uint32_t w, int i) {
-  if (F16) {
-    const uint32_t x = i == 0 ? w << 6 : (i == 1 ? w << 2 : (i == 2 ? w >> 2 : w >> 6));
-    return (x & 0x03c003c0u) | 0x3c003c00u;
-  }
   const uint32_t x = i == 0 ? w << 3 : w >> (4 * i - 3);
   return (x & 0x00780078u) | 0x3f803f80u;
+}
+// fp16 pairs from two shifts: 1 + code / 256 for nibbles 0 and 2, 1 + code / 16
+// for nibbles 1 and 3.
+__device__ __forceinline__ void code_pairs(uint32_t w, uint32_t (&v)[4]) {
+  const uint32_t x = w << 2, y = w >> 6;
+  v[0] = (x & 0x003c003cu) | 0x3c003c00u, v[1] = (x & 0x03c003c0u) | 0x3c003c00u;
+  v[2] = (y & 0x003c003cu) | 0x3c003c00u, v[3] = (y & 0x03c003c0u) | 0x3c003c00u;
 }
 // minus 1.5: (code - 8) / 16, exact
 __device__ __forceinline__ uint32_t centre(uint32_t v) {
@@ -146,6 +150,13 @@ __device__ __forceinline__ void codes_centred(uint32_t w, uint32_t (&v)[4]) {
   v[1] = as_u32(__hfma2(as_h2((w & 0x00f000f0u) | 0x64006400u), f, t));
   v[2] = as_u32(__hadd2(as_h2((x & 0x000f000fu) | 0x64006400u), k));
   v[3] = as_u32(__hfma2(as_h2((x & 0x00f000f0u) | 0x64006400u), f, t));
+}
+// D = A B (no sum in front).
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 __device__ __forceinline__ void mma_f16_k8(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b) {
   asm volatile(
@@ -168,7 +179,8 @@ __global__ void __launch_bounds__(32 * kWarps, 2) kv4_decode_kernel(const DecArg
   uint8_t *ring_all = smem;
   uint4 *qf = reinterpret_cast<uint4 *>(smem + S::kRing);             // [NS][NG][32]
   float *qs = reinterpret_cast<float *>(qf + NS * NG * 32);          // [NG][8]
-  float *qinv = qs + NG * 8;                                         // [8] inverse scale of a head's query
+  float *qd = qs + NG * 8;                                           // [NG][8] sums as the products take them
+  float *qinv = qd + NG * 8;                                         // [8] inverse scale of a head's query
   float2 *ml = reinterpret_cast<float2 *>(qinv + 8);                 // [kWarps][8] {m, l}
   uint64_t *bars = reinterpret_cast<uint64_t *>(ml + kWarps * 8);    // [kWarps][kStages]
   int64_t *scan = reinterpret_cast<int64_t *>(bars + kWarps * kStages);
@@ -264,7 +276,8 @@ __global__ void __launch_bounds__(32 * kWarps, 2) kv4_decode_kernel(const DecArg
       }
     };
     if (kHalf) {
-      // a warp per head; its largest element goes to 2^9, so that a group's sum stays below 2^14
+      // a warp per head; its largest element goes to 2^5, those at nibbles 0 and
+      // 2 sixteen times as high, so that a group's sums stay below 2^14
       const int rr = warp;
       float y[NG / 4][8], mx = 0.f;
 #pragma unroll
@@ -276,17 +289,23 @@ __global__ void __launch_bounds__(32 * kWarps, 2) kv4_decode_kernel(const DecArg
 #pragma unroll
       for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
       float inv;
-      const float s = scale_f16(mx, inv) * 0x1p-5f;
-      if (lane == 0) qinv[rr] = inv * 0x1p5f;
+      const float s = scale_f16(mx, inv) * 0x1p-9f;
+      if (lane == 0) qinv[rr] = inv * 0x1p9f;
 #pragma unroll
       for (int i = 0; i < NG / 4; ++i) {
         const int g = 4 * i + (lane >> 3), cc = (lane >> 1) & 3;
 #pragma unroll
         for (int e = 0; e < 8; ++e) y[i][e] *= s;
-        float sum = ((y[i][0] + y[i][1]) + (y[i][2] + y[i][3])) + ((y[i][4] + y[i][5]) + (y[i][6] + y[i][7]));
-        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 4);
-        if ((lane & 7) == 0) qs[g * 8 + rr] = sum;
+        // elements 0, 4, 2, 6 meet nibbles 0 and 2, elements 1, 5, 3, 7 nibbles 1 and 3
+        float far = (y[i][0] + y[i][4]) + (y[i][2] + y[i][6]), sum = (y[i][1] + y[i][5]) + (y[i][3] + y[i][7]);
+#pragma unroll
+        for (int o = 2; o <= 4; o <<= 1) {
+          far += __shfl_xor_sync(0xffffffffu, far, o);
+          sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        }
+        if ((lane & 7) == 0) qs[g * 8 + rr] = far + sum, qd[g * 8 + rr] = fmaf(16.f, far, sum);
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) y[i][e] *= 16.f;
         if ((lane & 1) == 0)  // pairs (0,4) (1,5) (2,6) (3,7): nibble i of both halves of a code word
           qf[g * 32 + rr * 4 + cc] = make_uint4(pack_f16(y[i][0], y[i][4]), pack_f16(y[i][1], y[i][5]),
                                                 pack_f16(y[i][2], y[i][6]), pack_f16(y[i][3], y[i][7]));
@@ -320,8 +339,8 @@ __global__ void __launch_bounds__(32 * kWarps, 2) kv4_decode_kernel(const DecArg
       to_log2 *= 16.f * qinv[r];
 #pragma unroll
       for (int i = 0; i < NG / 4; ++i) {
-        const float v = qs[(c + 4 * i) * 8 + r];
-        split_f16(-v, v * 0.0625f, ch[i], cl[i]);
+        const int at = (c + 4 * i) * 8 + r;
+        split_f16(-qd[at], qs[at] * 0.0625f, ch[i], cl[i]);
       }
     }
 
@@ -333,7 +352,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) kv4_decode_kernel(const DecArg
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[g][e][i] = 0.f;
     float m_run = -INFINITY, l_run = 0.f;  // of query head r; l over this thread's tokens
-    float room = kTop;  // log2 that p may reach: kTop less the largest log2 |d| met (16-bit types)
+    float room = kTop - 1.f;  // log2 that p may reach: kTop less that of the largest |d| met, 2 at least (16-bit types)
 
     for (int it = 0; it < n_it; ++it) {
       const int st = it % kStages;
@@ -369,18 +388,20 @@ __global__ void __launch_bounds__(32 * kWarps, 2) kv4_decode_kernel(const DecArg
         for (int gg = 0; gg < 4; ++gg) {
           const int g = gq * 4 + gg;
           uint32_t A0[4], A1[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) A0[i] = code_pair<kHalf>(wa[gg], i), A1[i] = code_pair<kHalf>(wb[gg], i);
           float x[4] = {0.f, 0.f, 0.f, 0.f};
           if (kHalf) {
+            code_pairs(wa[gg], A0);
+            code_pairs(wb[gg], A1);
             const uint4 b = qf[g * 32 + lane];
             const uint32_t p[4] = {A0[0], A1[0], A0[1], A1[1]}, q[4] = {A0[2], A1[2], A0[3], A1[3]};
-            mma_f16(x, p, b.x, b.y);
+            mma_f16_first(x, p, b.x, b.y);
             mma_f16(x, q, b.z, b.w);
             const float da = h_lo(ka[gg]), db = h_lo(kb[gg]);
             s[0] = fmaf(da, x[0], s[0]), s[1] = fmaf(da, x[1], s[1]);
             s[2] = fmaf(db, x[2], s[2]), s[3] = fmaf(db, x[3], s[3]);
           } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) A0[i] = code_pair(wa[gg], i), A1[i] = code_pair(wb[gg], i);
 #pragma unroll
             for (int p = 0; p < NS; ++p) {
               const uint4 b = qf[(p * NG + g) * 32 + lane];
@@ -416,7 +437,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) kv4_decode_kernel(const DecArg
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         tk[i] = 2 * c + (i & 1) + 8 * (i >> 1), on[i] = tk[i] < live;
-        p[i] = on[i] ? p[i] * to_log2 : -INFINITY;
+        p[i] *= to_log2;
         if (NG == 8) {
           const uint4 d = ptx::lds128(vs + tk[i] * 16);
           dw[i][0] = d.x, dw[i][1] = d.y, dw[i][NG / 2 - 2] = d.z, dw[i][NG / 2 - 1] = d.w;
@@ -427,25 +448,33 @@ __global__ void __launch_bounds__(32 * kWarps, 2) kv4_decode_kernel(const DecArg
       }
       if (live < 16) {  // what lies behind the sequence may be anything
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 4; ++i) {
+          p[i] = on[i] ? p[i] : -INFINITY;
 #pragma unroll
           for (int g = 0; g < NG / 2; ++g) dw[i][g] = on[i] ? dw[i][g] : 0u;
+        }
       }
       float mx = fmaxf(fmaxf(p[0], p[1]), fmaxf(p[2], p[3]));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
       if (kHalf) {
-        __half2 big = __habs2(as_h2(dw[0][0]));
+        uint32_t any = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int g = 0; g < NG / 2; ++g)
-            if (i + g > 0) big = __hmax2(big, __habs2(as_h2(dw[i][g])));
-        big = __hmax2(big, as_h2(__shfl_xor_sync(0xffffffffu, as_u32(big), 1)));
-        big = __hmax2(big, as_h2(__shfl_xor_sync(0xffffffffu, as_u32(big), 2)));
-        const float top = fmaxf(__low2float(big), __high2float(big));
-        // 2^n > top for n = exponent + 1; at most 16
-        if (top >= 1.f) room = fminf(room, kTop - (float)min(16, (int)(__float_as_uint(top) >> 23) - 126));
+          for (int g = 0; g < NG / 2; ++g) any |= dw[i][g];
+        if (__any_sync(0xffffffffu, any & 0x40004000u)) {  // a step of 2 or more (`room` starts one below for the rest)
+          __half2 big = __habs2(as_h2(dw[0][0]));
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int g = 0; g < NG / 2; ++g) big = __hmax2(big, __habs2(as_h2(dw[i][g])));
+          big = __hmax2(big, as_h2(__shfl_xor_sync(0xffffffffu, as_u32(big), 1)));
+          big = __hmax2(big, as_h2(__shfl_xor_sync(0xffffffffu, as_u32(big), 2)));
+          // 2^n > top for n = exponent + 1; at most 16
+          const float top = fmaxf(__low2float(big), __high2float(big));
+          room = fminf(room, kTop - (float)min(16, max(0, (int)(__float_as_uint(top) >> 23) - 126)));
+        }
       }
       // rescale only when a score passes the reference by 2^8 (16-bit types: by
       // what keeps p and p d in fp16) or the first one comes: the sums stay far
@@ -561,8 +590,8 @@ __global__ void __launch_bounds__(32 * kWarps, 2) kv4_decode_kernel(const DecArg
           const uint32_t Y = __byte_perm(vw[2][g >> 1], vw[3][g >> 1], sel);
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const uint32_t a0 = centre(code_pair<false>(X, 2 * e)), a1 = centre(code_pair<false>(X, 2 * e + 1));
-            const uint32_t a2 = centre(code_pair<false>(Y, 2 * e)), a3 = centre(code_pair<false>(Y, 2 * e + 1));
+            const uint32_t a0 = centre(code_pair(X, 2 * e)), a1 = centre(code_pair(X, 2 * e + 1));
+            const uint32_t a2 = centre(code_pair(Y, 2 * e)), a3 = centre(code_pair(Y, 2 * e + 1));
 #pragma unroll
             for (int i = 0; i < 3; ++i) mma_bf16(acc[g][e], a0, a1, a2, a3, ba[i], bb[i]);
           }
@@ -650,10 +679,12 @@ __global__ void __launch_bounds__(256) kv4_join_kernel(const DecArgs a) {
   __shared__ float run_l[kRuns];
   const int tid = threadIdx.x;
   const int seq = blockIdx.x / a.n_heads, head = blockIdx.x % a.n_heads;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int n_units = seq_units(a, seq);
   T *dst = (T *)a.out + (int64_t)seq * a.out_stride + (int64_t)head * D;
+  // the lengths are not the other kernel's to write: what they say is found
+  // while it still runs (but no block ends before it)
   if (n_units == 0) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (tid < D) dst[tid] = from_f32<T>(0.f);
     return;
   }
@@ -676,10 +707,11 @@ __global__ void __launch_bounds__(256) kv4_join_kernel(const DecArgs a) {
   // block of unit u: the i with total * i / parts <= u < total * (i + 1) / parts
   const int64_t parts = min((int64_t)a.grid, total);
   const int i0 = (int)(((u0 + 1) * parts - 1) / total), i1 = (int)(((u1 + 1) * parts - 1) / total);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (i0 == i1) return;  // one block saw all of it and wrote the output
   auto part = [&](int i) { return a.part + (int64_t)(2 * i + (i == i0 ? 1 : 0)) * kPart; };
   float m = -INFINITY;
-  for (int i = i0 + tid; i <= i1; i += blockDim.x) m = fmaxf(m, __ldg(part(i) + 8 * D + 2 * h));
+  for (int i = i0 + tid; i <= i1; i += blockDim.x) m = fmaxf(m, *(part(i) + 8 * D + 2 * h));
 #pragma unroll
   for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   if ((tid & 31) == 0) red[tid >> 5] = m;
@@ -693,8 +725,8 @@ __global__ void __launch_bounds__(256) kv4_join_kernel(const DecArgs a) {
 #pragma unroll 4
   for (int i = i0 + run; i <= i1; i += kRuns) {
     const float *p = part(i);
-    const float2 v = __ldg(reinterpret_cast<const float2 *>(p + 8 * D + 2 * h));
-    const float4 x = __ldg(reinterpret_cast<const float4 *>(p + h * D) + d4);
+    const float2 v = *reinterpret_cast<const float2 *>(p + 8 * D + 2 * h);
+    const float4 x = *(reinterpret_cast<const float4 *>(p + h * D) + d4);
     if (v.x > -INFINITY) {
       const float f = ex2(v.x - base);
       l = fmaf(f, v.y, l);
