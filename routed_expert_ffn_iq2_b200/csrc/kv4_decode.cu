@@ -25,7 +25,9 @@
 // Sums, maxima and the running softmax statistics are fp32.
 //
 // Split: the units of all sequences (128 tokens of one key/value head and up
-// to 8 of its query heads) form one list, cut evenly over a fixed grid; a
+// to 8 of its query heads; a sequence starts with kEntry units without tokens,
+// which stand for the time its first tiles and its result take) form one list,
+// cut evenly over a fixed grid; a
 // block joins its eight warps (16 tokens each, tiles streamed into a
 // per-warp ring by bulk copies) at the end of each run of units and writes
 // either the output or one of its two partial results, which kv4_join_kernel
@@ -37,6 +39,7 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kUnit = 16 * kWarps;  // tokens of a unit
+constexpr int kEntry = 4;           // units that a sequence counts for on top
 constexpr float kLazy = 8.f;        // log2 by which scores may pass the reference before sums are rescaled
 constexpr float kTop = 15.f;        // log2 that p, and p |d|, stay below in fp16
 
@@ -55,10 +58,11 @@ struct DecArgs {
   int32_t *status;
 };
 
+// Units of a sequence, the entry ones included (0: it has none).
 __device__ __forceinline__ int seq_units(const DecArgs &a, int s) {
   const int n = __ldg(a.lens + s);
   if (n <= 0 || (int64_t)n > (int64_t)a.max_pages * a.page_size) return 0;
-  return (n + kUnit - 1) / kUnit;
+  return (n + kUnit - 1) / kUnit + kEntry;
 }
 
 // Sum of the units of all sequences (of one head block), and where unit u of
@@ -221,8 +225,11 @@ __global__ void __launch_bounds__(32 * kWarps, 2) kv4_decode_kernel(const DecArg
       n_units = seq_units(a, ++seq);
     }
     const int64_t in_seq = u - seq_base * hh;
-    const int block_of = (int)(in_seq / n_units), j0 = (int)(in_seq % n_units);
-    const int j1 = (int)min((int64_t)n_units, j0 + (u_end - u));
+    const int block_of = (int)(in_seq / n_units), first = (int)(in_seq % n_units);
+    const int last = (int)min((int64_t)n_units, first + (u_end - u));
+    u += last - first;
+    const int j0 = max(0, first - kEntry), j1 = last - kEntry;  // units of tokens
+    if (j1 <= j0) continue;
     const int kvh = block_of / a.hb_count, hb = block_of % a.hb_count;
     const int len = __ldg(a.lens + seq);
     const int head0 = kvh * a.ratio + hb * 8, n_h = min(8, a.ratio - hb * 8);
@@ -630,7 +637,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) kv4_decode_kernel(const DecArg
           make_float4(acc[g][0][1] + g1, acc[g][0][3] + g1, acc[g][1][1] + g1, acc[g][1][3] + g1);
     }
     __syncthreads();
-    const bool whole = j0 == 0 && j1 == n_units;
+    const bool whole = j0 == 0 && j1 == n_units - kEntry;
     float *part = a.part + (int64_t)(2 * blockIdx.x + (j0 > 0 ? 0 : 1)) * (8 * D + 16);
     for (int i = tid; i < 8 * D / 4; i += 32 * kWarps) {
       const int h = i / (D / 4), d4 = i % (D / 4);
@@ -663,7 +670,6 @@ __global__ void __launch_bounds__(32 * kWarps, 2) kv4_decode_kernel(const DecArg
     }
     ptx::fence_proxy_async_smem();
     __syncthreads();
-    u += j1 - j0;
   }
 }
 
@@ -703,7 +709,8 @@ __global__ void __launch_bounds__(256) kv4_join_kernel(const DecArgs a) {
 #pragma unroll
   for (int w = 0; w < 8; ++w) before += front[w];
   const int kvh = head / a.ratio, in_kv = head % a.ratio, hb = in_kv >> 3, h = in_kv & 7;
-  const int64_t u0 = before * hh + (int64_t)(kvh * a.hb_count + hb) * n_units, u1 = u0 + n_units - 1;
+  const int64_t base_u = before * hh + (int64_t)(kvh * a.hb_count + hb) * n_units;
+  const int64_t u0 = base_u + kEntry, u1 = base_u + n_units - 1;  // units of tokens
   // block of unit u: the i with total * i / parts <= u < total * (i + 1) / parts
   const int64_t parts = min((int64_t)a.grid, total);
   const int i0 = (int)(((u0 + 1) * parts - 1) / total), i1 = (int)(((u1 + 1) * parts - 1) / total);
@@ -817,7 +824,8 @@ extern "C" int redlite_kv4_decode(int32_t dtype, const void *q, int64_t q_stride
   a.part = (float *)workspace;
   a.status = status;
   // no more blocks than units the longest lengths could give
-  const int64_t cap = (int64_t)n_seqs * n_kv_heads * a.hb_count * (((int64_t)max_pages * page_size + kUnit - 1) / kUnit);
+  const int64_t cap =
+      (int64_t)n_seqs * n_kv_heads * a.hb_count * (((int64_t)max_pages * page_size + kUnit - 1) / kUnit + kEntry);
   a.grid = (int)std::min<int64_t>(std::min(2 * sms, kMaxGrid), cap);
   cudaStream_t s = (cudaStream_t)stream;
   cudaError_t e;
