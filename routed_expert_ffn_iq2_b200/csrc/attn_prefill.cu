@@ -24,7 +24,11 @@
 //   warps 4 ..  softmax: thread = row.  Scores come out of tensor memory,
 //               probabilities go back over them in the inputs' type (that
 //               rounding, 2^-8 or 2^-11 of each p at most, is what the product's type
-//               asks for; l sums the unrounded p)
+//               asks for; l sums the unrounded p), half a row at a time: the
+//               second product starts on the first 64 keys
+// The exponential unit (4 lanes a cycle and scheduler) would take as long as
+// the products of D = 128, so a quarter of the exponentials are polynomials on
+// the multiply-add units.
 // Steps: D = 256, one row tile, two score buffers used in turn; D = 128, two
 // row tiles with a buffer and a softmax group each, in turn.
 //
@@ -65,7 +69,7 @@ struct Shape {
 };
 
 struct Bars {
-  uint64_t q_full, full[kRing], empty[kRing], s_full[2], p_full[2], o_full[2];
+  uint64_t q_full, full[kRing], empty[kRing], s_full[2], p_half[2], p_full[2], o_full[2];
   uint32_t tmem;
   int dead;
 };
@@ -92,12 +96,82 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t *v) {
       : "r"(taddr));
 }
 
+// Two fp32 operations at a time.
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+  return (uint64_t)__float_as_uint(x) | ((uint64_t)__float_as_uint(y) << 32);
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+  return make_float2(__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32)));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+// 2^x of two numbers up to 2^6 by a polynomial: x = n + f with |f| <= 1/2, 2^f
+// to 2^-18 (degree 4, the smallest relative error on the interval, by Remez
+// exchange), n added to the exponent.  Below -126 it stays at 2^-126; a NaN
+// becomes a number of 2^127 or more.
+__device__ __forceinline__ float2 ex2_poly(float2 x) {
+  float a, b;
+  asm("max.NaN.f32 %0, %1, 0fC2FC0000;" : "=f"(a) : "f"(x.x));
+  asm("max.NaN.f32 %0, %1, 0fC2FC0000;" : "=f"(b) : "f"(x.y));
+  const uint64_t z = pair(a, b), y = add2(z, pair(12582912.f, 12582912.f)),
+                 n = add2(y, pair(-12582912.f, -12582912.f)), f = fma2(n, pair(-1.f, -1.f), z);
+  uint64_t p = fma2(pair(0.009570102207362652f, 0.009570102207362652f), f, pair(0.05591785907745361f, 0.05591785907745361f));
+  p = fma2(p, f, pair(0.240247443318367f, 0.240247443318367f));
+  p = fma2(p, f, pair(0.6931217908859253f, 0.6931217908859253f));
+  p = fma2(p, f, pair(0.9999992847442627f, 0.9999992847442627f));
+  return make_float2(__uint_as_float((uint32_t)p + ((uint32_t)y << 23)),
+                     __uint_as_float((uint32_t)(p >> 32) + ((uint32_t)(y >> 32) << 23)));
+}
+
 // Descriptor of a tile whose rows run along K and whose 64-element row pieces
 // (128 bytes, swizzled) run along N: `lead` bytes between 64-column pieces,
 // 1024 between groups of 8 rows.
 __device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t addr, uint32_t lead) {
   return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)((lead >> 4) & 0x3FFFu) << 16) | ((uint64_t)(1024 >> 4) << 32) |
          ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+// D[tmem] (+)= A B, issued by the one thread of a converged warp whose `go` is
+// set; descriptors as low and high word.  The whole warp walks the loop, so
+// that addresses stay in uniform registers: issued from a branch that one
+// thread takes, each product cost 110 cycles of moves into them, against the
+// 64 that it runs.
+template <bool ACC>
+__device__ __forceinline__ void umma_ss(uint32_t go, uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo,
+                                        uint32_t b_hi, uint32_t idesc) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 da, db;\n setp.ne.b32 p, %7, 0;\n mov.b64 da, {%1, %2};\n mov.b64 db, {%3, %4};\n"
+      " @p tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %5, %6;\n}\n" ::"r"(d),
+      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "n"(ACC ? 1 : 0), "r"(go)
+      : "memory");
+}
+__device__ __forceinline__ void umma_ts(uint32_t go, uint32_t d, uint32_t a, uint32_t b_lo, uint32_t b_hi,
+                                        uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n .reg .b64 db;\n setp.ne.b32 q, %6, 0;\n setp.ne.b32 p, %5, 0;\n mov.b64 db, {%2, %3};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate), "r"(go)
+      : "memory");
+}
+__device__ __forceinline__ void umma_done(uint32_t go, uint64_t *bar) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %1, 0;\n"
+      " @p tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(ptx::smem_u32(bar)),
+      "r"(go)
+      : "memory");
+}
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r;
 }
 
 // Bounded wait; after one that gave up every later one returns at once.
@@ -187,7 +261,8 @@ __global__ void __launch_bounds__(32 * Shape<D>::kWarps, 1)
     ptx::mbar_init(&b->q_full, 1);
     for (int i = 0; i < kRing; ++i) ptx::mbar_init(b->full + i, 1), ptx::mbar_init(b->empty + i, 1);
     for (int i = 0; i < 2; ++i)
-      ptx::mbar_init(b->s_full + i, 1), ptx::mbar_init(b->p_full + i, 128), ptx::mbar_init(b->o_full + i, 1);
+      ptx::mbar_init(b->s_full + i, 1), ptx::mbar_init(b->p_half + i, 128), ptx::mbar_init(b->p_full + i, 128),
+          ptx::mbar_init(b->o_full + i, 1);
     b->dead = 0;
     ptx::mbar_fence_init();
   }
@@ -244,76 +319,87 @@ __global__ void __launch_bounds__(32 * Shape<D>::kWarps, 1)
         if (i + 1 < n_tiles) load_k(i + 1);
       }
     }
-  } else if (warp == 1 && lane == 0 && n_tiles > 0) {
+  } else if (warp == 1 && n_tiles > 0) {
     // ============================================================= products
     constexpr uint32_t fmt = kBf ? ((1u << 7) | (1u << 10)) : 0u;
     constexpr uint32_t id_s = (1u << 4) | fmt | ((kKeys >> 3) << 17) | ((128u >> 4) << 24);
     constexpr uint32_t id_o = (1u << 4) | fmt | (1u << 16) | ((uint32_t)(D >> 3) << 17) | ((128u >> 4) << 24);
-    const uint32_t q_addr = ptx::smem_u32(sq), r_addr = ptx::smem_u32(ring);
-    int st = 0;         // ring stage of the next K or V tile
+    const uint64_t dq = ptx::sdesc_k_sw128(ptx::smem_u32(sq)), dk = ptx::sdesc_k_sw128(ptx::smem_u32(ring)),
+                   dv = sdesc_mn_sw128(ptx::smem_u32(ring), kKeys / kSub * 128);
+    const uint32_t q_lo = (uint32_t)dq, k_lo = (uint32_t)dk, v_lo = (uint32_t)dv, q_hi = (uint32_t)(dq >> 32),
+                   k_hi = (uint32_t)(dk >> 32), v_hi = (uint32_t)(dv >> 32);
+    // (reductions: the compiler knows their results to be uniform)
+    const uint32_t tm = __reduce_max_sync(0xffffffffu, tmem), steps = __reduce_max_sync(0xffffffffu, (uint32_t)n_tiles);
+    const uint32_t go = elect_one();
+    uint32_t st = 0;  // ring stage of the next K or V tile
     uint32_t ph = 0;
-    auto stage_wait = [&](int s, uint32_t p) { wait(b, b->full + s, p, a.status); };
+    auto warp_wait = [&](uint64_t *bar, uint32_t parity) {
+      wait(b, bar, parity, a.status);
+      __syncwarp();
+      ptx::tc_fence_after();
+    };
     // scores of one row tile: K tile in stages s ..
-    auto scores = [&](int row_tile, int buf, int s, uint32_t p, bool release) {
+    auto scores = [&](uint32_t row_tile, uint32_t buf, uint32_t s, uint32_t p, bool release) {
+#pragma unroll
       for (int h = 0; h < kSub; ++h) {
-        stage_wait(s, p);
-        ptx::tc_fence_after();
+        warp_wait(b->full + s, p);
+        const uint32_t ql = q_lo + (row_tile * (D / 64) + 2 * h) * (16384 >> 4), kl = k_lo + s * (kStageBytes >> 4);
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk) {
-          const uint64_t da = ptx::sdesc_k_sw128(q_addr + (row_tile * (D / 64) + 2 * h + kk / 4) * 16384 + (kk % 4) * 32);
-          const uint64_t db = ptx::sdesc_k_sw128(r_addr + s * kStageBytes + (kk / 4) * 16384 + (kk % 4) * 32);
-          ptx::umma_bf16(tmem + 128 * buf, da, db, id_s, h > 0 || kk > 0);
+          const uint32_t off = ((kk / 4) * 16384 + (kk % 4) * 32) >> 4;
+          if (kk > 0 || h > 0) umma_ss<true>(go, tm + 128 * buf, ql + off, q_hi, kl + off, k_hi, id_s);
+          else umma_ss<false>(go, tm + 128 * buf, ql + off, q_hi, kl + off, k_hi, id_s);
         }
-        if (release) ptx::umma_commit(b->empty + s);
+        if (release) umma_done(go, b->empty + s);
         if (++s == kRing) s = 0, p ^= 1;
       }
-      ptx::umma_commit(b->s_full + buf);
+      umma_done(go, b->s_full + buf);
     };
-    auto outputs = [&](int buf, int acc, int s, uint32_t p, bool first, bool release) {
+    auto outputs = [&](uint32_t buf, uint32_t acc, uint32_t s, uint32_t p, bool first, bool release, uint32_t turn) {
       constexpr int kRows = kKeys / kSub;
+#pragma unroll
       for (int h = 0; h < kSub; ++h) {
-        stage_wait(s, p);
-        ptx::tc_fence_after();
+        warp_wait(b->full + s, p);
 #pragma unroll
         for (int kk = 0; kk < kRows / 16; ++kk) {
-          const uint64_t dv = sdesc_mn_sw128(r_addr + s * kStageBytes + kk * 2048, kRows * 128);
-          ptx::umma_bf16_ts(tmem + Sh::kO + 128 * acc, tmem + 128 * buf + (h * kRows + kk * 16) / 2, dv, id_o,
-                            !first || h > 0 || kk > 0);
+          // the first or second 64 keys' probabilities
+          if (kk % 4 == 0) warp_wait(h * kRows + kk * 16 < 64 ? b->p_half + buf : b->p_full + buf, turn);
+          umma_ts(go, tm + Sh::kO + 128 * acc, tm + 128 * buf + (h * kRows + kk * 16) / 2,
+                  v_lo + s * (kStageBytes >> 4) + kk * (2048 >> 4), v_hi, id_o, !first || h > 0 || kk > 0);
         }
-        if (release) ptx::umma_commit(b->empty + s);
+        if (release) umma_done(go, b->empty + s);
         if (++s == kRing) s = 0, p ^= 1;
       }
-      ptx::umma_commit(b->o_full + acc);
+      umma_done(go, b->o_full + acc);
     };
-    auto skip = [&](int &s, uint32_t &p) {
+    auto skip = [&](uint32_t &s, uint32_t &p) {
       s += kSub;
       if (s >= kRing) s -= kRing, p ^= 1;
     };
-    wait(b, &b->q_full, 0, a.status);
+    auto gave_up = [&]() { return __any_sync(0xffffffffu, *(volatile int *)&b->dead); };
+    warp_wait(&b->q_full, 0);
     if (NQ == 1) {
       scores(0, 0, st, ph, true);
       skip(st, ph);
-      for (int i = 0; i < n_tiles && !*(volatile int *)&b->dead; ++i) {
-        if (i + 1 < n_tiles) {
+      for (uint32_t i = 0; i < steps && !gave_up(); ++i) {
+        if (i + 1 < steps) {
           scores(0, (i + 1) & 1, st, ph, true);
           skip(st, ph);
         }
-        wait(b, b->p_full + (i & 1), (i >> 1) & 1, a.status);
-        outputs(i & 1, 0, st, ph, i == 0, true);
+        outputs(i & 1, 0, st, ph, i == 0, true, (i >> 1) & 1);
         skip(st, ph);
       }
     } else {
       scores(0, 0, st, ph, false);
       scores(1, 1, st, ph, true);
       skip(st, ph);
-      for (int i = 0; i < n_tiles && !*(volatile int *)&b->dead; ++i) {
-        int s2 = st;  // V tile of this step, then K tile of the next
-        uint32_t p2 = ph;
+      for (uint32_t i = 0; i < steps && !gave_up(); ++i) {
+        uint32_t s2 = st, p2 = ph;  // V tile of this step, then K tile of the next
         skip(s2, p2);
-        for (int t = 0; t < 2; ++t) {
-          wait(b, b->p_full + t, i & 1, a.status);
-          outputs(t, t, st, ph, i == 0, t == 1);
-          if (i + 1 < n_tiles) scores(t, t, s2, p2, t == 1);
+#pragma unroll
+        for (uint32_t t = 0; t < 2; ++t) {
+          outputs(t, t, st, ph, i == 0, t == 1, i & 1);
+          if (i + 1 < steps) scores(t, t, s2, p2, t == 1);
         }
         skip(st, ph);
         skip(st, ph);
@@ -345,7 +431,8 @@ __global__ void __launch_bounds__(32 * Shape<D>::kWarps, 1)
       }
       float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int j = 0; j < kKeys; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(s[j]));
+      for (int j = 0; j < kKeys; j += 2)
+        mx[(j >> 1) & 3] = fmaxf(fmaxf(mx[(j >> 1) & 3], __uint_as_float(s[j])), __uint_as_float(s[j + 1]));
       const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
       if (__any_sync(0xffffffffu, top > m + kLazy || (m == -INFINITY && top > -INFINITY))) {
         const float mn = fmaxf(m, top);
@@ -369,23 +456,26 @@ __global__ void __launch_bounds__(32 * Shape<D>::kWarps, 1)
         }
       }
       const float neg = m == -INFINITY ? 0.f : -m;
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      const uint64_t neg2 = pair(neg, neg), scale2 = pair(a.scale_log2, a.scale_log2);
+      uint64_t sum[2] = {0, 0};
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint32_t p[32];
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
-          const float x = ex2(fmaf(__uint_as_float(s[64 * h + 2 * j]), a.scale_log2, neg));
-          const float y = ex2(fmaf(__uint_as_float(s[64 * h + 2 * j + 1]), a.scale_log2, neg));
-          sum[(2 * j) & 3] += x, sum[(2 * j + 1) & 3] += y;
-          p[j] = kBf ? pack_bf16(x, y) : pack_f16(x, y);
+          const float2 z = unpair(fma2(pair(__uint_as_float(s[64 * h + 2 * j]), __uint_as_float(s[64 * h + 2 * j + 1])),
+                                       scale2, neg2));
+          const float2 e = (j & 3) == 3 ? ex2_poly(z) : make_float2(ex2(z.x), ex2(z.y));
+          sum[j & 1] = add2(sum[j & 1], pair(e.x, e.y));
+          p[j] = kBf ? pack_bf16(e.x, e.y) : pack_f16(e.x, e.y);
         }
         ptx::tmem_st32x32b_x32(t_s + 32 * h, p);
+        ptx::tmem_wait_st();
+        ptx::tc_fence_before();
+        ptx::mbar_arrive((h == 0 ? b->p_half : b->p_full) + buf);
       }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-      ptx::tmem_wait_st();
-      ptx::tc_fence_before();
-      ptx::mbar_arrive(b->p_full + buf);
+      const float2 both = unpair(add2(sum[0], sum[1]));
+      l += both.x + both.y;
     }
     // ---- rows out
     T *dst = (T *)a.out + (int64_t)(q0 + tok) * a.out_stride + (int64_t)head * D;
@@ -395,7 +485,7 @@ __global__ void __launch_bounds__(32 * Shape<D>::kWarps, 1)
       __syncwarp();
       ptx::tc_fence_after();
     }
-    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+    const float inv = m > -INFINITY ? 1.f / l : 0.f;  // no key was seen: 0
 #pragma unroll 1
     for (int d = 0; d < D; d += 32) {
       uint32_t o[32];
