@@ -11,26 +11,24 @@
 // Both products run on the tensor cores (tcgen05, fp32 accumulators in tensor
 // memory), 4 D flops per visible pair, which is the bound: a tile of 128 rows
 // by 128 keys takes 2 x 128 x 128 x D multiply-adds against 128 x 128
-// exponentials.  One block per 128 rows (D = 256) or 2 x 128 rows (D = 128);
-// the rows of a tile are tokens x the query heads that share a key/value head
-// (the largest power of two G of them), so keys are read once for G heads and
-// a prompt of a few tokens still fills its tile.
+// exponentials.  One block per 128 rows, and two of them on a multiprocessor
+// where heads are 128 wide (then in steps of 64 keys); the rows of a tile are
+// tokens x the query heads that share a key/value head (the largest power of
+// two G of them), so keys are read once for G heads and a prompt of a few
+// tokens still fills its tile.
 //   warp 0      one thread: TMA loads of Q (once) and of K and V in a ring of
-//               five 32 KB stages (128B-swizzled boxes)
-//   warp 1      one thread: issues the products.  Scores of step i + 1 are
-//               issued in front of the second product of step i, so the
-//               tensor cores work while the softmax does
+//               stages (128B-swizzled boxes)
+//   warp 1      issues the products.  Two score buffers are used in turn: the
+//               scores of step i + 1 are issued in front of the second product
+//               of step i, so the tensor cores work while the softmax does
 //   warp 2      tensor memory allocation
 //   warps 4 ..  softmax: thread = row.  Scores come out of tensor memory,
 //               probabilities go back over them in the inputs' type (that
 //               rounding, 2^-8 or 2^-11 of each p at most, is what the product's type
 //               asks for; l sums the unrounded p), half a row at a time: the
-//               second product starts on the first 64 keys
-// The exponential unit (4 lanes a cycle and scheduler) would take as long as
-// the products of D = 128, so a quarter of the exponentials are polynomials on
-// the multiply-add units.
-// Steps: D = 256, one row tile, two score buffers used in turn; D = 128, two
-// row tiles with a buffer and a softmax group each, in turn.
+//               second product starts on the first half of the keys
+// A block's start and end (loads, first scores, rows out: 7 us) go by beside
+// the other block's steps where there are two.
 //
 // A zero probability times a NaN or an infinity in V is a NaN that a masked
 // key must not cause: a row whose result is not finite is computed again by
@@ -54,28 +52,33 @@ struct AttnArgs {
   int32_t *status;
 };
 
-constexpr int kKeys = 128;          // keys per step
-constexpr int kStageBytes = 32768;  // 128 keys x 128 values (K), or 64 x 256 / 128 x 128 (V)
-constexpr int kRing = 5;
-constexpr int kQBytes = 65536;
+constexpr int kRows = 128;          // rows of a tile
 constexpr float kLazy = 8.f;
 
 template <int D>
 struct Shape {
-  static constexpr int NQ = D == 128 ? 2 : 1;   // row tiles per block
-  static constexpr int kSub = D / 128;          // stages per K or V tile
-  static constexpr int kWarps = 4 + 4 * NQ;
-  static constexpr uint32_t kO = 256;           // first accumulator column of O (scores: 0 and 128)
+  static constexpr int kBlocks = D == 128 ? 2 : 1;         // on a multiprocessor
+  static constexpr int kKeys = D == 128 ? 64 : 128;        // keys per step
+  static constexpr int kSub = kKeys / 64;                  // stages per K or V tile
+  static constexpr int kStageBytes = 64 * D * 2;           // kKeys keys x 128 values (K) or 64 x D (V)
+  static constexpr int kRing = D == 128 ? 4 : 5;
+  static constexpr int kQBytes = kRows * D * 2;
+  static constexpr uint32_t kO = 2 * kKeys;                // first accumulator column of O, behind the scores
+  static constexpr uint32_t kColumns = kO + D;
+  static_assert(kKeys * 128 * 2 == kStageBytes, "K and V stages are of one size");
 };
 
+template <int D>
 struct Bars {
-  uint64_t q_full, full[kRing], empty[kRing], s_full[2], p_half[2], p_full[2], o_full[2];
+  uint64_t q_full, full[Shape<D>::kRing], empty[Shape<D>::kRing], s_full[2], p_half[2], p_full[2], o_full;
   uint32_t tmem;
   int dead;
 };
-
-constexpr int kSmem = kQBytes + kRing * kStageBytes + (int)sizeof(Bars) + 1024;
-static_assert(kSmem <= 227 * 1024, "shared memory of a block");
+template <int D>
+constexpr int attn_smem() {
+  return Shape<D>::kQBytes + Shape<D>::kRing * Shape<D>::kStageBytes + (int)sizeof(Bars<D>) + 1024;
+}
+static_assert(attn_smem<256>() <= 227 * 1024 && 2 * (attn_smem<128>() + 1024) <= 228 * 1024, "shared memory of a block");
 
 __device__ __forceinline__ void tma_load3(void *dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar) {
   asm volatile(
@@ -113,22 +116,12 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
-// 2^x of two numbers up to 2^6 by a polynomial: x = n + f with |f| <= 1/2, 2^f
-// to 2^-18 (degree 4, the smallest relative error on the interval, by Remez
-// exchange), n added to the exponent.  Below -126 it stays at 2^-126; a NaN
-// becomes a number of 2^127 or more.
-__device__ __forceinline__ float2 ex2_poly(float2 x) {
-  float a, b;
-  asm("max.NaN.f32 %0, %1, 0fC2FC0000;" : "=f"(a) : "f"(x.x));
-  asm("max.NaN.f32 %0, %1, 0fC2FC0000;" : "=f"(b) : "f"(x.y));
-  const uint64_t z = pair(a, b), y = add2(z, pair(12582912.f, 12582912.f)),
-                 n = add2(y, pair(-12582912.f, -12582912.f)), f = fma2(n, pair(-1.f, -1.f), z);
-  uint64_t p = fma2(pair(0.009570102207362652f, 0.009570102207362652f), f, pair(0.05591785907745361f, 0.05591785907745361f));
-  p = fma2(p, f, pair(0.240247443318367f, 0.240247443318367f));
-  p = fma2(p, f, pair(0.6931217908859253f, 0.6931217908859253f));
-  p = fma2(p, f, pair(0.9999992847442627f, 0.9999992847442627f));
-  return make_float2(__uint_as_float((uint32_t)p + ((uint32_t)y << 23)),
-                     __uint_as_float((uint32_t)(p >> 32) + ((uint32_t)(y >> 32) << 23)));
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
 }
 
 // Descriptor of a tile whose rows run along K and whose 64-element row pieces
@@ -175,7 +168,8 @@ __device__ __forceinline__ uint32_t elect_one() {
 }
 
 // Bounded wait; after one that gave up every later one returns at once.
-__device__ __forceinline__ bool wait(Bars *b, uint64_t *bar, uint32_t parity, int32_t *status) {
+template <int D>
+__device__ __forceinline__ bool wait(Bars<D> *b, uint64_t *bar, uint32_t parity, int32_t *status) {
   if (ptx::mbar_try_wait(bar, parity)) return true;
   if (*(volatile int *)&b->dead) return false;
   if (ptx::mbar_wait_suspend(bar, parity)) return true;
@@ -218,58 +212,61 @@ __device__ __noinline__ void row_again(const AttnArgs &a, int64_t q_row, int hea
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(32 * Shape<D>::kWarps, 1)
+__global__ void __launch_bounds__(256, Shape<D>::kBlocks)
     attn_prefill_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                         const __grid_constant__ CUtensorMap mv, const AttnArgs a) {
   using Sh = Shape<D>;
-  constexpr int NQ = Sh::NQ, kSub = Sh::kSub;
+  constexpr int kKeys = Sh::kKeys, kSub = Sh::kSub, kRing = Sh::kRing, kStageBytes = Sh::kStageBytes;
   constexpr bool kBf = sizeof(T) == 2 && std::is_same<T, __nv_bfloat16>::value;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((1024 - (ptx::smem_u32(smem_raw) & 1023)) & 1023);
-  uint8_t *sq = smem, *ring = smem + kQBytes;
-  Bars *b = reinterpret_cast<Bars *>(ring + kRing * kStageBytes);
+  uint8_t *sq = smem, *ring = smem + Sh::kQBytes;
+  Bars<D> *b = reinterpret_cast<Bars<D> *>(ring + kRing * kStageBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+  if (threadIdx.x == 0) {
+    for (const CUtensorMap *m : {&mq, &mk, &mv}) asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
+    ptx::mbar_init(&b->q_full, 1);
+    for (int i = 0; i < kRing; ++i) ptx::mbar_init(b->full + i, 1), ptx::mbar_init(b->empty + i, 1);
+    for (int i = 0; i < 2; ++i)
+      ptx::mbar_init(b->s_full + i, 1), ptx::mbar_init(b->p_half + i, 128), ptx::mbar_init(b->p_full + i, 128);
+    ptx::mbar_init(&b->o_full, 1);
+    b->dead = 0;
+    ptx::mbar_fence_init();
+  }
+  if (warp == 2) {
+    ptx::tmem_alloc(&b->tmem, Sh::kColumns);
+    ptx::tmem_relinquish();
+  }
   if (blockIdx.x == 0)
     for (int s = threadIdx.x; s < a.n_seqs; s += blockDim.x) {
       const int b0 = __ldg(a.cu_q + s), e0 = __ldg(a.cu_q + s + 1), b1 = __ldg(a.cu_k + s), e1 = __ldg(a.cu_k + s + 1);
       if (b0 < 0 || e0 < b0 || e0 > a.n_q || b1 < 0 || e1 < b1 || e1 > a.n_k) set_status(a.status, REDLITE_STATUS_BAD_LENGTH);
     }
-  // ---- which rows: the last tiles of the last sequences first (most keys)
-  const int tile_tok = kKeys >> a.log_group, block_tok = NQ * tile_tok;
+  // ---- which rows: the last tiles of the last sequences first (most keys).
+  // The sequence is the last whose first slot is not behind this one: 32
+  // places are looked at together.
+  const int tile_tok = kRows >> a.log_group;
   const int hb = blockIdx.x % (a.n_heads >> a.log_group);
   const int64_t slot = (gridDim.x - 1 - blockIdx.x) / (a.n_heads >> a.log_group);
-  int lo = 0, hi = a.n_seqs;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if ((int64_t)(__ldg(a.cu_q + mid) / block_tok) + mid <= slot) lo = mid;
-    else hi = mid;
+  int lo = 0;
+  for (int n = a.n_seqs; n > 1;) {  // it is one of lo .. lo + n - 1
+    const int step = (n + 31) >> 5, at = lo + lane * step;
+    const bool in = lane * step < n && (int64_t)(__ldg(a.cu_q + at) / tile_tok) + at <= slot;
+    const uint32_t found = __ballot_sync(0xffffffffu, in) | 1u;
+    const int skip = (31 - __clz(found)) * step;
+    lo += skip, n = min(step, n - skip);
   }
   const int q0 = __ldg(a.cu_q + lo), q1 = __ldg(a.cu_q + lo + 1), k0 = __ldg(a.cu_k + lo), k1 = __ldg(a.cu_k + lo + 1);
   const bool valid = q0 >= 0 && q1 >= q0 && q1 <= a.n_q && k0 >= 0 && k1 >= k0 && k1 <= a.n_k;
-  if (!valid) return;
-  const int64_t t0l = (slot - ((int64_t)(q0 / block_tok) + lo)) * block_tok;
+  const int64_t t0l = (slot - ((int64_t)(q0 / tile_tok) + lo)) * tile_tok;
   const int q_len = q1 - q0, k_len = k1 - k0;
-  if (t0l < 0 || t0l >= q_len) return;
-  const int t0 = (int)t0l;
+  const bool work = valid && t0l >= 0 && t0l < q_len;
+  const int t0 = work ? (int)t0l : 0;
   const int shift = k_len - q_len;  // query t sees keys 0 .. t + shift
-  const int lim_max = max(0, min(q_len, t0 + block_tok) + shift);
+  const int lim_max = work ? max(0, min(q_len, t0 + tile_tok) + shift) : 0;
   const int n_tiles = (lim_max + kKeys - 1) / kKeys;
   const int head0 = hb << a.log_group, kh = head0 / (a.n_heads / a.n_kv);
-
-  if (threadIdx.x == 0) {
-    ptx::mbar_init(&b->q_full, 1);
-    for (int i = 0; i < kRing; ++i) ptx::mbar_init(b->full + i, 1), ptx::mbar_init(b->empty + i, 1);
-    for (int i = 0; i < 2; ++i)
-      ptx::mbar_init(b->s_full + i, 1), ptx::mbar_init(b->p_half + i, 128), ptx::mbar_init(b->p_full + i, 128),
-          ptx::mbar_init(b->o_full + i, 1);
-    b->dead = 0;
-    ptx::mbar_fence_init();
-  }
-  if (warp == 2) {
-    ptx::tmem_alloc(&b->tmem, 512);
-    ptx::tmem_relinquish();
-  }
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
@@ -277,10 +274,6 @@ __global__ void __launch_bounds__(32 * Shape<D>::kWarps, 1)
 
   if (warp == 0 && lane == 0 && n_tiles > 0) {
     // ================================================================ loads
-    ptx::mbar_expect_tx(&b->q_full, kQBytes);
-    for (int t = 0; t < NQ; ++t)
-      for (int d = 0; d < D / 64; ++d)
-        tma_load3(sq + (t * (D / 64) + d) * 16384, &mq, 64 * d, head0, q0 + t0 + t * tile_tok, &b->q_full);
     int st = 0;
     uint32_t ph = 1;  // parity with which an empty stage is waited for (the first round passes)
     auto next = [&]() -> uint8_t * {  // null once a wait gave up: no copy is started any more
@@ -292,40 +285,37 @@ __global__ void __launch_bounds__(32 * Shape<D>::kWarps, 1)
       if (++st == kRing) st = 0, ph ^= 1;
     };
     auto load_k = [&](int i) {
-      for (int h = 0; h < kSub; ++h) {
+      for (int h = 0; h < D / 128; ++h) {
         uint8_t *dst = next();
         if (!dst) return;
-        for (int d = 0; d < 2; ++d) tma_load3(dst + d * 16384, &mk, 128 * h + 64 * d, kh, k0 + i * kKeys, b->full + st);
+        for (int d = 0; d < 2; ++d)
+          tma_load3(dst + d * kKeys * 128, &mk, 128 * h + 64 * d, kh, k0 + i * kKeys, b->full + st);
         step();
       }
     };
     auto load_v = [&](int i) {
-      constexpr int kRows = kKeys / kSub;
       for (int h = 0; h < kSub; ++h) {
         uint8_t *dst = next();
         if (!dst) return;
         for (int d = 0; d < D / 64; ++d)
-          tma_load3(dst + d * kRows * 128, &mv, 64 * d, kh, k0 + i * kKeys + h * kRows, b->full + st);
+          tma_load3(dst + d * 8192, &mv, 64 * d, kh, k0 + i * kKeys + h * 64, b->full + st);
         step();
       }
     };
+    ptx::mbar_expect_tx(&b->q_full, Sh::kQBytes);
+    for (int d = 0; d < D / 64; ++d) tma_load3(sq + d * 16384, &mq, 64 * d, head0, q0 + t0, &b->q_full);
     load_k(0);
     for (int i = 0; i < n_tiles && !*(volatile int *)&b->dead; ++i) {
-      if (NQ == 1) {
-        if (i + 1 < n_tiles) load_k(i + 1);
-        load_v(i);
-      } else {
-        load_v(i);
-        if (i + 1 < n_tiles) load_k(i + 1);
-      }
+      if (i + 1 < n_tiles) load_k(i + 1);
+      load_v(i);
     }
   } else if (warp == 1 && n_tiles > 0) {
     // ============================================================= products
     constexpr uint32_t fmt = kBf ? ((1u << 7) | (1u << 10)) : 0u;
-    constexpr uint32_t id_s = (1u << 4) | fmt | ((kKeys >> 3) << 17) | ((128u >> 4) << 24);
+    constexpr uint32_t id_s = (1u << 4) | fmt | ((uint32_t)(kKeys >> 3) << 17) | ((128u >> 4) << 24);
     constexpr uint32_t id_o = (1u << 4) | fmt | (1u << 16) | ((uint32_t)(D >> 3) << 17) | ((128u >> 4) << 24);
     const uint64_t dq = ptx::sdesc_k_sw128(ptx::smem_u32(sq)), dk = ptx::sdesc_k_sw128(ptx::smem_u32(ring)),
-                   dv = sdesc_mn_sw128(ptx::smem_u32(ring), kKeys / kSub * 128);
+                   dv = sdesc_mn_sw128(ptx::smem_u32(ring), 8192);
     const uint32_t q_lo = (uint32_t)dq, k_lo = (uint32_t)dk, v_lo = (uint32_t)dv, q_hi = (uint32_t)(dq >> 32),
                    k_hi = (uint32_t)(dk >> 32), v_hi = (uint32_t)(dv >> 32);
     // (reductions: the compiler knows their results to be uniform)
@@ -338,101 +328,85 @@ __global__ void __launch_bounds__(32 * Shape<D>::kWarps, 1)
       __syncwarp();
       ptx::tc_fence_after();
     };
-    // scores of one row tile: K tile in stages s ..
-    auto scores = [&](uint32_t row_tile, uint32_t buf, uint32_t s, uint32_t p, bool release) {
+    auto step = [&]() {
+      if (++st == kRing) st = 0, ph ^= 1;
+    };
+    auto scores = [&](uint32_t buf) {
 #pragma unroll
-      for (int h = 0; h < kSub; ++h) {
-        warp_wait(b->full + s, p);
-        const uint32_t ql = q_lo + (row_tile * (D / 64) + 2 * h) * (16384 >> 4), kl = k_lo + s * (kStageBytes >> 4);
+      for (int h = 0; h < D / 128; ++h) {
+        warp_wait(b->full + st, ph);
+        const uint32_t ql = q_lo + 2 * h * (16384 >> 4), kl = k_lo + st * (kStageBytes >> 4);
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk) {
-          const uint32_t off = ((kk / 4) * 16384 + (kk % 4) * 32) >> 4;
-          if (kk > 0 || h > 0) umma_ss<true>(go, tm + 128 * buf, ql + off, q_hi, kl + off, k_hi, id_s);
-          else umma_ss<false>(go, tm + 128 * buf, ql + off, q_hi, kl + off, k_hi, id_s);
+          const uint32_t oq = ((kk / 4) * 16384 + (kk % 4) * 32) >> 4, ok = ((kk / 4) * kKeys * 128 + (kk % 4) * 32) >> 4;
+          if (kk > 0 || h > 0) umma_ss<true>(go, tm + kKeys * buf, ql + oq, q_hi, kl + ok, k_hi, id_s);
+          else umma_ss<false>(go, tm + kKeys * buf, ql + oq, q_hi, kl + ok, k_hi, id_s);
         }
-        if (release) umma_done(go, b->empty + s);
-        if (++s == kRing) s = 0, p ^= 1;
+        umma_done(go, b->empty + st);
+        step();
       }
       umma_done(go, b->s_full + buf);
     };
-    auto outputs = [&](uint32_t buf, uint32_t acc, uint32_t s, uint32_t p, bool first, bool release, uint32_t turn) {
-      constexpr int kRows = kKeys / kSub;
+    auto outputs = [&](uint32_t buf, bool first, uint32_t turn) {
 #pragma unroll
       for (int h = 0; h < kSub; ++h) {
-        warp_wait(b->full + s, p);
+        warp_wait(b->full + st, ph);
 #pragma unroll
-        for (int kk = 0; kk < kRows / 16; ++kk) {
-          // the first or second 64 keys' probabilities
-          if (kk % 4 == 0) warp_wait(h * kRows + kk * 16 < 64 ? b->p_half + buf : b->p_full + buf, turn);
-          umma_ts(go, tm + Sh::kO + 128 * acc, tm + 128 * buf + (h * kRows + kk * 16) / 2,
-                  v_lo + s * (kStageBytes >> 4) + kk * (2048 >> 4), v_hi, id_o, !first || h > 0 || kk > 0);
+        for (int kk = 0; kk < 4; ++kk) {
+          // the first or second half of the keys' probabilities
+          const int key = 64 * h + 16 * kk;
+          if (key % (kKeys / 2) == 0) warp_wait(key == 0 ? b->p_half + buf : b->p_full + buf, turn);
+          umma_ts(go, tm + Sh::kO, tm + kKeys * buf + key / 2, v_lo + st * (kStageBytes >> 4) + kk * (2048 >> 4), v_hi, id_o,
+                  !first || key > 0);
         }
-        if (release) umma_done(go, b->empty + s);
-        if (++s == kRing) s = 0, p ^= 1;
+        umma_done(go, b->empty + st);
+        step();
       }
-      umma_done(go, b->o_full + acc);
+      umma_done(go, &b->o_full);
     };
-    auto skip = [&](uint32_t &s, uint32_t &p) {
-      s += kSub;
-      if (s >= kRing) s -= kRing, p ^= 1;
-    };
-    auto gave_up = [&]() { return __any_sync(0xffffffffu, *(volatile int *)&b->dead); };
     warp_wait(&b->q_full, 0);
-    if (NQ == 1) {
-      scores(0, 0, st, ph, true);
-      skip(st, ph);
-      for (uint32_t i = 0; i < steps && !gave_up(); ++i) {
-        if (i + 1 < steps) {
-          scores(0, (i + 1) & 1, st, ph, true);
-          skip(st, ph);
-        }
-        outputs(i & 1, 0, st, ph, i == 0, true, (i >> 1) & 1);
-        skip(st, ph);
-      }
-    } else {
-      scores(0, 0, st, ph, false);
-      scores(1, 1, st, ph, true);
-      skip(st, ph);
-      for (uint32_t i = 0; i < steps && !gave_up(); ++i) {
-        uint32_t s2 = st, p2 = ph;  // V tile of this step, then K tile of the next
-        skip(s2, p2);
-#pragma unroll
-        for (uint32_t t = 0; t < 2; ++t) {
-          outputs(t, t, st, ph, i == 0, t == 1, i & 1);
-          if (i + 1 < steps) scores(t, t, s2, p2, t == 1);
-        }
-        skip(st, ph);
-        skip(st, ph);
-      }
+    scores(0);
+    for (uint32_t i = 0; i < steps && !__any_sync(0xffffffffu, *(volatile int *)&b->dead); ++i) {
+      if (i + 1 < steps) scores((i + 1) & 1);
+      outputs(i & 1, i == 0, (i >> 1) & 1);
     }
-  } else if (warp >= 4) {
+  } else if (warp >= 4 && work) {
     // ============================================================== softmax
-    const int wg = (warp - 4) >> 2, row = 32 * (warp & 3) + lane;
-    const int tok = t0 + wg * tile_tok + (row >> a.log_group), head = head0 + (row & (a.group - 1));
+    const int row0 = 32 * (warp & 3), row = row0 + lane;
+    const int tok = t0 + (row >> a.log_group), head = head0 + (row & (a.group - 1));
     const bool mine = tok < q_len;
     const int lim = mine ? max(0, tok + shift + 1) : 0;
-    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-    const uint32_t t_o = tmem + lanes + Sh::kO + 128 * wg;
+    const uint32_t lanes = (uint32_t)row0 << 16;
+    const uint32_t t_o = tmem + lanes + Sh::kO;
+    const uint64_t scale2 = pair(a.scale_log2, a.scale_log2);
     float m = -INFINITY, l = 0.f;
     for (int i = 0; i < n_tiles && !*(volatile int *)&b->dead; ++i) {
-      const int buf = NQ == 1 ? (i & 1) : wg;
-      const uint32_t t_s = tmem + lanes + 128 * buf;
-      wait(b, b->s_full + buf, NQ == 1 ? (i >> 1) & 1 : i & 1, a.status);
+      const int buf = i & 1;
+      const uint32_t t_s = tmem + lanes + kKeys * buf;
+      wait(b, b->s_full + buf, (i >> 1) & 1, a.status);
       __syncwarp();
       ptx::tc_fence_after();
-      uint32_t s[kKeys];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) tmem_ld32(t_s + 32 * j, s + 32 * j);
-      ptx::tmem_wait_ld();
+      constexpr int kHalf = kKeys / 2;
+      uint32_t s[kHalf];  // one half's scores at a time
       const int left = lim - i * kKeys;  // keys of this tile that the row sees
-      if (__any_sync(0xffffffffu, left < kKeys)) {
+      const bool edge = __any_sync(0xffffffffu, left < kKeys);
+      auto load = [&](int h) {
 #pragma unroll
-        for (int j = 0; j < kKeys; ++j) s[j] = j < left ? s[j] : 0xff800000u;
-      }
+        for (int j = 0; j < kHalf; j += 32) tmem_ld32(t_s + kHalf * h + j, s + j);
+        ptx::tmem_wait_ld();
+        if (edge) {
+#pragma unroll
+          for (int j = 0; j < kHalf; ++j) s[j] = kHalf * h + j < left ? s[j] : 0xff800000u;
+        }
+      };
       float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int j = 0; j < kKeys; j += 2)
-        mx[(j >> 1) & 3] = fmaxf(fmaxf(mx[(j >> 1) & 3], __uint_as_float(s[j])), __uint_as_float(s[j + 1]));
+      for (int h = 1; h >= 0; --h) {
+        load(h);
+#pragma unroll
+        for (int j = 0; j < kHalf; j += 2)
+          mx[(j >> 1) & 3] = fmaxf(fmaxf(mx[(j >> 1) & 3], __uint_as_float(s[j])), __uint_as_float(s[j + 1]));
+      }
       const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
       if (__any_sync(0xffffffffu, top > m + kLazy || (m == -INFINITY && top > -INFINITY))) {
         const float mn = fmaxf(m, top);
@@ -441,7 +415,7 @@ __global__ void __launch_bounds__(32 * Shape<D>::kWarps, 1)
         l *= f;
         if (i > 0) {
           // the product of the step in front has to be in
-          wait(b, b->o_full + (NQ == 1 ? 0 : wg), (i - 1) & 1, a.status);
+          wait(b, &b->o_full, (i - 1) & 1, a.status);
           __syncwarp();
           ptx::tc_fence_after();
 #pragma unroll 1
@@ -456,20 +430,22 @@ __global__ void __launch_bounds__(32 * Shape<D>::kWarps, 1)
         }
       }
       const float neg = m == -INFINITY ? 0.f : -m;
-      const uint64_t neg2 = pair(neg, neg), scale2 = pair(a.scale_log2, a.scale_log2);
+      const uint64_t neg2 = pair(neg, neg);
       uint64_t sum[2] = {0, 0};
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        uint32_t p[32];
+        if (h) load(h);
+        uint32_t p[kHalf / 2];
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const float2 z = unpair(fma2(pair(__uint_as_float(s[64 * h + 2 * j]), __uint_as_float(s[64 * h + 2 * j + 1])),
-                                       scale2, neg2));
-          const float2 e = (j & 3) == 3 ? ex2_poly(z) : make_float2(ex2(z.x), ex2(z.y));
-          sum[j & 1] = add2(sum[j & 1], pair(e.x, e.y));
-          p[j] = kBf ? pack_bf16(e.x, e.y) : pack_f16(e.x, e.y);
+        for (int j = 0; j < kHalf / 2; ++j) {
+          const float2 z = unpair(fma2(pair(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])), scale2, neg2));
+          const float x = ex2(z.x), y = ex2(z.y);
+          sum[j & 1] = add2(sum[j & 1], pair(x, y));
+          p[j] = kBf ? pack_bf16(x, y) : pack_f16(x, y);
         }
-        ptx::tmem_st32x32b_x32(t_s + 32 * h, p);
+        // over scores that are in registers or done with
+#pragma unroll
+        for (int j = 0; j < kHalf / 2; j += 16) tmem_st16(t_s + kHalf / 2 * h + j, p + j);
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
         ptx::mbar_arrive((h == 0 ? b->p_half : b->p_full) + buf);
@@ -477,15 +453,17 @@ __global__ void __launch_bounds__(32 * Shape<D>::kWarps, 1)
       const float2 both = unpair(add2(sum[0], sum[1]));
       l += both.x + both.y;
     }
-    // ---- rows out
-    T *dst = (T *)a.out + (int64_t)(q0 + tok) * a.out_stride + (int64_t)head * D;
+    // ---- rows out, through the warp's part of Q's place (the products that
+    // read it are done), so that a store covers whole rows
     bool odd = false;
     if (n_tiles > 0) {
-      wait(b, b->o_full + (NQ == 1 ? 0 : wg), (n_tiles - 1) & 1, a.status);
+      wait(b, &b->o_full, (n_tiles - 1) & 1, a.status);
       __syncwarp();
       ptx::tc_fence_after();
     }
-    const float inv = m > -INFINITY ? 1.f / l : 0.f;  // no key was seen: 0
+    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+    constexpr int kPieces = D / 8;  // of 16 bytes in a row
+    uint8_t *mine_out = sq + row0 * D * 2;
 #pragma unroll 1
     for (int d = 0; d < D; d += 32) {
       uint32_t o[32];
@@ -502,12 +480,22 @@ __global__ void __launch_bounds__(32 * Shape<D>::kWarps, 1)
         float x[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(o[8 * j + e]) * inv, chk = fmaf(x[e], 0.f, chk);
-        if (mine) store8<T>(dst + d + 8 * j, x);
+        store8<T>(reinterpret_cast<T *>(mine_out + lane * D * 2 + (((d / 8 + j) ^ (lane & 7)) << 4)), x);
       }
       odd = odd || !(chk == 0.f);
     }
+    __syncwarp();
+#pragma unroll 4
+    for (int i = 0; i < kPieces; ++i) {
+      const int id = i * 32 + lane, r = id / kPieces, piece = id % kPieces;
+      const int t = t0 + ((row0 + r) >> a.log_group), hd = head0 + ((row0 + r) & (a.group - 1));
+      const uint4 v = *reinterpret_cast<const uint4 *>(mine_out + r * D * 2 + ((piece ^ (r & 7)) << 4));
+      if (t < q_len)
+        *reinterpret_cast<uint4 *>((T *)a.out + (int64_t)(q0 + t) * a.out_stride + (int64_t)hd * D + piece * 8) = v;
+    }
     ptx::tc_fence_before();
     uint32_t again = __ballot_sync(0xffffffffu, odd && mine);
+    __syncwarp();  // the rows are written: an odd one is written again
     while (again) {
       const int src = __ffs(again) - 1;
       again &= again - 1;
@@ -518,7 +506,7 @@ __global__ void __launch_bounds__(32 * Shape<D>::kWarps, 1)
   }
   __syncthreads();
   ptx::tc_fence_after();
-  if (warp == 2) ptx::tmem_dealloc(tmem, 512);
+  if (warp == 2) ptx::tmem_dealloc(tmem, Sh::kColumns);
 }
 
 typedef CUresult (*EncodeTiled)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
@@ -554,22 +542,20 @@ bool make_map(CUtensorMap *m, int32_t dtype, const void *p, int64_t stride, int6
 template <typename T, int D>
 int launch_attn(const AttnArgs &a, int32_t dtype, cudaStream_t s) {
   CUtensorMap mq, mk, mv;
-  const int tile_tok = kKeys >> a.log_group;
-  constexpr int v_rows = kKeys / Shape<D>::kSub;
+  const int tile_tok = kRows >> a.log_group;
   // without keys no K or V box is loaded; the maps still need an address
   const void *k = a.n_k > 0 ? a.k : a.q, *v = a.n_k > 0 ? a.v : a.q;
   const int64_t ks = a.n_k > 0 ? a.k_stride : a.q_stride, vs = a.n_k > 0 ? a.v_stride : a.q_stride;
   const int hk = a.n_k > 0 ? a.n_kv : a.n_heads;
   const int64_t nk = a.n_k > 0 ? a.n_k : a.n_q;
   if (!make_map(&mq, dtype, a.q, a.q_stride, a.n_q, a.n_heads, D, a.group, tile_tok) ||
-      !make_map(&mk, dtype, k, ks, nk, hk, D, 1, kKeys) || !make_map(&mv, dtype, v, vs, nk, hk, D, 1, v_rows))
+      !make_map(&mk, dtype, k, ks, nk, hk, D, 1, Shape<D>::kKeys) || !make_map(&mv, dtype, v, vs, nk, hk, D, 1, 64))
     return REDLITE_ECUDA;
-  if (cudaFuncSetAttribute(attn_prefill_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
+  if (cudaFuncSetAttribute(attn_prefill_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, attn_smem<D>()) != cudaSuccess)
     return REDLITE_ECUDA;
-  const int block_tok = Shape<D>::NQ * tile_tok;
-  const int64_t grid = ((int64_t)a.n_q / block_tok + a.n_seqs) * (a.n_heads >> a.log_group);
+  const int64_t grid = ((int64_t)a.n_q / tile_tok + a.n_seqs) * (a.n_heads >> a.log_group);
   if (grid >= ((int64_t)1 << 31) - 1) return REDLITE_EUNSUPPORTED;
-  attn_prefill_kernel<T, D><<<(unsigned)grid, 32 * Shape<D>::kWarps, kSmem, s>>>(mq, mk, mv, a);
+  attn_prefill_kernel<T, D><<<(unsigned)grid, 256, attn_smem<D>(), s>>>(mq, mk, mv, a);
   return cudaGetLastError() == cudaSuccess ? REDLITE_OK : REDLITE_ECUDA;
 }
 
