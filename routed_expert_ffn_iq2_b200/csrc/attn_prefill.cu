@@ -224,6 +224,7 @@ __global__ void __launch_bounds__(256, Shape<D>::kBlocks)
   Bars<D> *b = reinterpret_cast<Bars<D> *>(ring + kRing * kStageBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+  after_predecessor();
   if (threadIdx.x == 0) {
     for (const CUtensorMap *m : {&mq, &mk, &mv}) asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
     ptx::mbar_init(&b->q_full, 1);
@@ -555,8 +556,9 @@ int launch_attn(const AttnArgs &a, int32_t dtype, cudaStream_t s) {
     return REDLITE_ECUDA;
   const int64_t grid = ((int64_t)a.n_q / tile_tok + a.n_seqs) * (a.n_heads >> a.log_group);
   if (grid >= ((int64_t)1 << 31) - 1) return REDLITE_EUNSUPPORTED;
-  attn_prefill_kernel<T, D><<<(unsigned)grid, 256, attn_smem<D>(), s>>>(mq, mk, mv, a);
-  return cudaGetLastError() == cudaSuccess ? REDLITE_OK : REDLITE_ECUDA;
+  return launch_early(attn_prefill_kernel<T, D>, (unsigned)grid, 256, attn_smem<D>(), s, mq, mk, mv, a) == cudaSuccess
+             ? REDLITE_OK
+             : REDLITE_ECUDA;
 }
 
 }  // namespace

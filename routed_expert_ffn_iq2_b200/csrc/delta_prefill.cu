@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(256, 2) delta_prep_kernel(const DeltaArgs a, c
   __shared__ float2 sc[2][C];  // sums of log2 decays: high and low part
   __shared__ float snk[C], snq[C], sss[2][C], sb[2][C];
   __shared__ __align__(16) float td[2][4][16 * kPitchT];
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  after_predecessor();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, c = lane & 3;
   if (blockIdx.x == 0)
     order_sequences(a, reinterpret_cast<int32_t *>(a.ws + w.order), reinterpret_cast<int *>(smem));
@@ -595,9 +595,7 @@ __global__ void __launch_bounds__(32 * (2 * kChains + 1), 1) delta_chain_kernel(
     }
   }
   ptx::mbar_fence_init();
-  // in front of every way out: this grid must not end before the one that
-  // writes the workspace
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  after_predecessor();
   int seq = blockIdx.x / (slices * a.n_v);
   if (ordered) seq = *reinterpret_cast<const int32_t *>(a.ws + w.order + 4 * (size_t)seq);
   const int64_t slot = delta_slot(a, seq);
@@ -931,24 +929,14 @@ cudaError_t launch_prefill(const DeltaArgs &a, const WsPlan &w, cudaStream_t s) 
     constexpr int smem = prep_smem<NK, DK>();
     e = cudaFuncSetAttribute(delta_prep_kernel<T, NK, DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    delta_prep_kernel<T, NK, DK>
-        <<<(unsigned)(chunk_slots(a.n_tokens, a.n_seqs) * a.n_k), 256, smem, s>>>(a, w);
-    e = cudaGetLastError();
+    e = launch_early(delta_prep_kernel<T, NK, DK>, (unsigned)(chunk_slots(a.n_tokens, a.n_seqs) * a.n_k), 256, smem, s, a, w);
     if (e != cudaSuccess) return e;
   }
   constexpr int smem = Chain<T, NK, DK>::kSmem;
   e = cudaFuncSetAttribute(delta_chain_kernel<T, NK, DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((int64_t)a.n_seqs * a.n_v * (a.dv / kCols)));
-  cfg.blockDim = dim3(32 * (2 * kChains + 1));
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at, cfg.numAttrs = a.n_tokens > 0 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, delta_chain_kernel<T, NK, DK>, a, w, a.n_tokens > 0);
+  return launch_early(delta_chain_kernel<T, NK, DK>, (unsigned)((int64_t)a.n_seqs * a.n_v * (a.dv / kCols)),
+                      32 * (2 * kChains + 1), smem, s, a, w, a.n_tokens > 0);
 }
 
 template <typename T, int NK>

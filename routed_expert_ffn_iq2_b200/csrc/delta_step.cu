@@ -43,6 +43,7 @@ constexpr int kStepCols = 32;
 
 template <typename T, int DK>
 __global__ void __launch_bounds__(128) delta_step_kernel(const DeltaArgs a) {
+  after_predecessor();
   constexpr int kRows = DK / 16;  // state rows per thread
   __shared__ float sk[DK], sq[DK];
   __shared__ float red[3][4];
@@ -137,9 +138,7 @@ __global__ void __launch_bounds__(128) delta_step_kernel(const DeltaArgs a) {
 template <typename T>
 cudaError_t launch_step(const DeltaArgs &a, cudaStream_t s) {
   const unsigned grid = (unsigned)((int64_t)a.n_seqs * a.n_v * (a.dv / kStepCols));
-  if (a.dk == 128) delta_step_kernel<T, 128><<<grid, 128, 0, s>>>(a);
-  else delta_step_kernel<T, 64><<<grid, 128, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_early(a.dk == 128 ? delta_step_kernel<T, 128> : delta_step_kernel<T, 64>, grid, 128, 0, s, a);
 }
 
 }  // namespace

@@ -122,6 +122,7 @@ __device__ __forceinline__ uint32_t quantise(const float (&x)[8], __half &dh, __
 
 template <typename T, int D>
 __global__ void __launch_bounds__(256) kv4_append_kernel(const Kv4Args a) {
+  after_predecessor();
   const Rows<D> row(a);
   const int w = threadIdx.x % Rows<D>::kWords, g = w >> 2, c = w & 3;
   // a row's threads share these conditions, and the shuffles stay inside
@@ -158,6 +159,7 @@ __device__ __forceinline__ void expand(uint32_t word, float d, float m, float (&
 
 template <typename T, int D>
 __global__ void __launch_bounds__(256) kv4_load_kernel(const Kv4Args a) {
+  after_predecessor();
   const Rows<D> row(a);
   if (!row.live) return;
   const int w = threadIdx.x % Rows<D>::kWords, g = w >> 2, c = w & 3;
@@ -187,14 +189,8 @@ template <bool APPEND, typename T>
 cudaError_t launch_rows(const Kv4Args &a, int D, cudaStream_t s) {
   const int64_t per = a.n_heads, rows = 256 / (D / 8), tokens = per < rows ? rows / per : 1;
   const dim3 grid((unsigned)((a.n_tokens + tokens - 1) / tokens), (unsigned)((per + rows - 1) / rows));
-  if (D == 256) {
-    if (APPEND) kv4_append_kernel<T, 256><<<grid, 256, 0, s>>>(a);
-    else kv4_load_kernel<T, 256><<<grid, 256, 0, s>>>(a);
-  } else {
-    if (APPEND) kv4_append_kernel<T, 128><<<grid, 256, 0, s>>>(a);
-    else kv4_load_kernel<T, 128><<<grid, 256, 0, s>>>(a);
-  }
-  return cudaGetLastError();
+  if (D == 256) return launch_early(APPEND ? kv4_append_kernel<T, 256> : kv4_load_kernel<T, 256>, grid, 256, 0, s, a);
+  return launch_early(APPEND ? kv4_append_kernel<T, 128> : kv4_load_kernel<T, 128>, grid, 256, 0, s, a);
 }
 
 template <bool APPEND>

@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) kv4_decode_kernel(const DecArg
   uint64_t *bars = reinterpret_cast<uint64_t *>(ml + kWarps * 8);    // [kWarps][kStages]
   int64_t *scan = reinterpret_cast<int64_t *>(bars + kWarps * kStages);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, c = lane & 3;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  after_predecessor();  // (the joining kernel reads lengths as soon as this has returned everywhere)
   uint64_t *bar = bars + warp * kStages;
   uint8_t *ring = ring_all + warp * kStages * S::kTile;
   if (lane == 0)
@@ -690,7 +690,7 @@ __global__ void __launch_bounds__(256) kv4_join_kernel(const DecArgs a) {
   // the lengths are not the other kernel's to write: what they say is found
   // while it still runs (but no block ends before it)
   if (n_units == 0) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    after_predecessor();
     if (tid < D) dst[tid] = from_f32<T>(0.f);
     return;
   }
@@ -714,7 +714,7 @@ __global__ void __launch_bounds__(256) kv4_join_kernel(const DecArgs a) {
   // block of unit u: the i with total * i / parts <= u < total * (i + 1) / parts
   const int64_t parts = min((int64_t)a.grid, total);
   const int i0 = (int)(((u0 + 1) * parts - 1) / total), i1 = (int)(((u1 + 1) * parts - 1) / total);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  after_predecessor();
   if (i0 == i1) return;  // one block saw all of it and wrote the output
   auto part = [&](int i) { return a.part + (int64_t)(2 * i + (i == i0 ? 1 : 0)) * kPart; };
   float m = -INFINITY;
@@ -761,18 +761,9 @@ cudaError_t launch_decode(const DecArgs &a, cudaStream_t s) {
   cudaError_t e =
       cudaFuncSetAttribute(kv4_decode_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  kv4_decode_kernel<T, D><<<a.grid, 32 * kWarps, smem, s>>>(a);
-  e = cudaGetLastError();
+  e = launch_early(kv4_decode_kernel<T, D>, a.grid, 32 * kWarps, smem, s, a);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(a.n_seqs * a.n_heads));
-  cfg.blockDim = dim3(256);
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at, cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv4_join_kernel<T, D>, a);
+  return launch_early(kv4_join_kernel<T, D>, (unsigned)(a.n_seqs * a.n_heads), 256, 0, s, a);
 }
 template <typename T>
 cudaError_t launch_decode_t(const DecArgs &a, int D, cudaStream_t s) {
