@@ -70,7 +70,7 @@ struct Shape {
 
 template <int D>
 struct Bars {
-  uint64_t q_full, full[Shape<D>::kRing], empty[Shape<D>::kRing], s_full[2], p_half[2], p_full[2], o_full;
+  uint64_t q_full, full[Shape<D>::kRing], empty[Shape<D>::kRing], s_full[2], p_half[2], p_full[2], o_full, done;
   uint32_t tmem;
   int dead;
 };
@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(256, Shape<D>::kBlocks)
     for (int i = 0; i < kRing; ++i) ptx::mbar_init(b->full + i, 1), ptx::mbar_init(b->empty + i, 1);
     for (int i = 0; i < 2; ++i)
       ptx::mbar_init(b->s_full + i, 1), ptx::mbar_init(b->p_half + i, 128), ptx::mbar_init(b->p_full + i, 128);
-    ptx::mbar_init(&b->o_full, 1);
+    ptx::mbar_init(&b->o_full, 1), ptx::mbar_init(&b->done, 1);
     b->dead = 0;
     ptx::mbar_fence_init();
   }
@@ -368,9 +368,18 @@ __global__ void __launch_bounds__(256, Shape<D>::kBlocks)
     warp_wait(&b->q_full, 0);
     scores(0);
     for (uint32_t i = 0; i < steps && !__any_sync(0xffffffffu, *(volatile int *)&b->dead); ++i) {
-      if (i + 1 < steps) scores((i + 1) & 1);
+      if (i + 1 < steps) {
+        // their buffer holds the probabilities of step i - 1: the product that
+        // reads those has to be through (products of different accumulators
+        // keep no order of their own)
+        if (i > 0) warp_wait(&b->o_full, (i - 1) & 1);
+        scores((i + 1) & 1);
+      }
       outputs(i & 1, i == 0, (i >> 1) & 1);
     }
+    // (a row may come to its end two products ahead: o_full's parity would not
+    // tell the last product from the one before the last)
+    umma_done(go, &b->done);
   } else if (warp >= 4 && work) {
     // ============================================================== softmax
     const int row0 = 32 * (warp & 3), row = row0 + lane;
@@ -458,7 +467,7 @@ __global__ void __launch_bounds__(256, Shape<D>::kBlocks)
     // read it are done), so that a store covers whole rows
     bool odd = false;
     if (n_tiles > 0) {
-      wait(b, &b->o_full, (n_tiles - 1) & 1, a.status);
+      wait(b, &b->done, 0, a.status);
       __syncwarp();
       ptx::tc_fence_after();
     }

@@ -229,6 +229,36 @@ def test_streams_graphs_strides(P):
 
 
 @gpu
+@pytest.mark.parametrize("t,D,Hq,Hk,lens", [(torch.float16, 128, 32, 8, [1000, 513, 0, 2047, 64, 333]),
+                                            (torch.bfloat16, 128, 8, 8, [1, 200, 900]),
+                                            (torch.bfloat16, 256, 16, 2, [700, 65, 1500, 128]),
+                                            (torch.float16, 256, 4, 4, [300, 1, 800])])
+def test_many_blocks_give_the_same_bits_every_time(P, t, D, Hq, Hk, lens):
+    """Blocks that share multiprocessors, thirty times: nothing depends on how they fall, and rows of the ends of
+    their tiles (the last keys are the last product's) are right."""
+    rng = np.random.default_rng(D + Hq)
+    n = sum(lens)
+    q, k, v = _inputs(rng, t, n, n, Hq, Hk, D)
+    cu = R.cu(lens)
+    first = torch.empty_like(q)
+    assert P.redlite_attn_prefill(q, k, v, cu, cu, first, 2 * D ** -0.5) == P.REDLITE_OK
+    hq, hk, hv = _host(q), _host(k), _host(v)
+    at = 0
+    for m in lens:
+        for i in sorted({0, m // 2, m - 17, m - 1} & set(range(m))):
+            # the last query of a sequence cut off behind i sees what query i sees
+            ref, lim = _reference(hq[at + i:at + i + 1], hk[at:at + i + 1], hv[at:at + i + 1], [1], [i + 1],
+                                  2 * D ** -0.5, t)
+            _check(first[at + i:at + i + 1], ref, lim)
+        at += m
+    out = torch.empty_like(q)
+    for _ in range(30):
+        out.fill_(9.0)
+        assert P.redlite_attn_prefill(q, k, v, cu, cu, out, 2 * D ** -0.5) == P.REDLITE_OK
+        assert torch.equal(out, first)
+
+
+@gpu
 def test_strided_rows_past_32_bits(P):
     """Rows of a joint tensor so wide that element offsets pass 2^31."""
     T, W = 40, 1 << 26
