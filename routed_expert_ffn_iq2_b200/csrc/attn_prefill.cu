@@ -28,7 +28,14 @@
 //               asks for; l sums the unrounded p), half a row at a time: the
 //               second product starts on the first half of the keys
 // A block's start and end (loads, first scores, rows out: 7 us) go by beside
-// the other block's steps where there are two.
+// the other block's steps where there are two (one block of two row tiles, a
+// softmax group each: 82 us for the ragged batch below).
+//
+// Measured (one B200): 16384 tokens, 16 heads on 2 of 256, bf16: 1.62 to 1.73 ms,
+// 1.27 to 1.36 PFLOP/s (a long library product: 1.39); five ragged fp16 prompts,
+// 3957 tokens of 32 heads on 8 of 128: 73 us, 650 TFLOP/s; three of 43 tokens
+// together 8.1 us.  Tried without gain: two threads a row in the softmax,
+// polynomials for a part of the exponentials.
 //
 // A zero probability times a NaN or an infinity in V is a NaN that a masked
 // key must not cause: a row whose result is not finite is computed again by
@@ -277,13 +284,14 @@ __global__ void __launch_bounds__(256, Shape<D>::kBlocks)
     // ================================================================ loads
     int st = 0;
     uint32_t ph = 1;  // parity with which an empty stage is waited for (the first round passes)
+    bool first_round = true;
     auto next = [&]() -> uint8_t * {  // null once a wait gave up: no copy is started any more
       if (!wait(b, b->empty + st, ph, a.status)) return nullptr;
       ptx::mbar_expect_tx(b->full + st, kStageBytes);
       return ring + st * kStageBytes;
     };
     auto step = [&]() {
-      if (++st == kRing) st = 0, ph ^= 1;
+      if (++st == kRing) st = 0, ph ^= 1, first_round = false;
     };
     auto load_k = [&](int i) {
       for (int h = 0; h < D / 128; ++h) {
@@ -309,6 +317,12 @@ __global__ void __launch_bounds__(256, Shape<D>::kBlocks)
     for (int i = 0; i < n_tiles && !*(volatile int *)&b->dead; ++i) {
       if (i + 1 < n_tiles) load_k(i + 1);
       load_v(i);
+    }
+    // after a wait that gave up: what is on its way still lands in this block
+    if (*(volatile int *)&b->dead) {
+      ptx::mbar_wait_suspend(&b->q_full, 0);
+      for (int s = 0; s < kRing; ++s)
+        if (s < st || !first_round) ptx::mbar_wait_suspend(b->full + s, s < st ? ph ^ 1 : ph);
     }
   } else if (warp == 1 && n_tiles > 0) {
     // ============================================================= products

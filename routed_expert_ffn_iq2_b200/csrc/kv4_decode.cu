@@ -32,6 +32,14 @@
 // per-warp ring by bulk copies) at the end of each run of units and writes
 // either the output or one of its two partial results, which kv4_join_kernel
 // adds up in a fixed order: no atomics, nothing kept from call to call.
+//
+// Measured (one B200, floor at 6550 GB/s in brackets): 16 contexts of 49k to
+// 66k tokens, 32 heads on 8 of 128, fp16: 320 us, 3.7 TB/s [180 us]; 64 ragged
+// contexts up to 8k, 16 heads on 2 of 256, bf16: 60 us [24 us]; one of 700
+// tokens, fp32: 12 us.  What bounds the long case is instructions: 467 a tile
+// of 16 tokens of 128, half of them on the integer units (which take one every
+// other cycle), with 16 warps a multiprocessor (128 registers, what the
+// accumulators leave).
 #include "kv4.cuh"
 
 namespace redlite {
@@ -39,7 +47,10 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kUnit = 16 * kWarps;  // tokens of a unit
-constexpr int kEntry = 4;           // units that a sequence counts for on top
+// Units that a sequence counts for on top: with none, a block of many short
+// sequences ran 30% longer than the rest (64 ragged contexts: 71 us; 4: 62 us;
+// 8: 68 us).
+constexpr int kEntry = 4;
 constexpr float kLazy = 8.f;        // log2 by which scores may pass the reference before sums are rescaled
 constexpr float kTop = 15.f;        // log2 that p, and p |d|, stay below in fp16
 
