@@ -403,8 +403,8 @@ int redlite_attn_prefill(int32_t dtype, const void *q, int64_t q_stride, const v
 size_t redlite_kv4_page_bytes(int32_t n_kv_heads, int32_t head_dim, int32_t page_size);
 
 /* Store the new tokens' keys and values: row cu[s] + i of k and v becomes
- * token start[s] + i of sequence s.  start: device int32 [n_seqs].  Of two
- * rows that a call maps to one place, one is stored (which one is open). */
+ * token start[s] + i of sequence s.  start: device int32 [n_seqs].  What a
+ * place holds after a call that maps two rows to it is open. */
 int redlite_kv4_append(int32_t dtype, const void *k, const void *v, int64_t k_stride, int64_t v_stride,
                        const int32_t *cu_tokens, const int32_t *start, int32_t n_seqs, int32_t n_tokens,
                        int32_t n_kv_heads, int32_t head_dim, int32_t page_size, const int32_t *block_table,
@@ -419,8 +419,10 @@ int redlite_kv4_load(int32_t dtype, const void *cache, int32_t n_kv_heads, int32
 
 /* Attention of one query per sequence over its cached tokens:
  *   out[s, h] = sum_{t < lens[s]} softmax_t(scale * q[s, h] . K[t, kh]) V[t, kh]
- * K, V the values the cache stands for, used unrounded.  lens: device int32
- * [n_seqs]; a sequence of length 0 gives zeros, and so does one whose length
+ * K, V the values the cache stands for, never rounded themselves; with 16-bit
+ * activations a probability and its product with a group's step d are rounded
+ * to fp16 (relative to p d code that is 2^-10 at most, of either sign).
+ * lens: device int32 [n_seqs]; a sequence of length 0 gives zeros, and so does one whose length
  * is negative or beyond max_pages * page_size (reported); tokens on a page
  * that is not in the cache are left out (reported).
  *   q, out   device [n_seqs rows, n_heads * head_dim]
@@ -455,7 +457,8 @@ int redlite_kv4_decode(int32_t dtype, const void *q, int64_t q_stride, int32_t n
  * redlite_delta_prefill runs packed sequences of any lengths in chunks of 64
  * tokens (with n_tokens = 0 it copies the states); workspace 256-byte
  * aligned.  A cu that does not ascend within 0 .. n_tokens is reported; the
- * sequences it breaks are skipped, their states not written.
+ * sequences it breaks are skipped, their states not written, and what the
+ * others give is open (nothing out of range is read or written).
  * redlite_delta_step runs one token per sequence: row s is sequence s. */
 size_t redlite_delta_workspace_bytes(int32_t n_tokens, int32_t n_seqs, int32_t n_k_heads, int32_t n_v_heads, int32_t dk,
                                      int32_t dv);

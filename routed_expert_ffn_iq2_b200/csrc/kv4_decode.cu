@@ -17,9 +17,11 @@
 // (that needs no shift of its own), the query's element is 16 times as large.
 // Two forms of the rest:
 //   16-bit activations  a head's query scaled by a power of two into one fp16
-//               part (exact); p d is one fp16 product (2^-11 of each term at
-//               most, below what the outputs' type rounds).  The reference of
-//               the softmax is kept so that neither p nor p d leaves fp16:
+//               part (exact); p and p d are rounded to fp16 (2^-10 of each
+//               term's p d (code - 8) in all at most, of either sign; the sum
+//               over p m and the softmax's own sum keep p whole).  The
+//               reference of the softmax is kept so that neither p nor p d
+//               leaves fp16:
 //               p <= 2^15 / max(1, |d|) for the largest |d| met so far.
 //   fp32        the query in three bf16 parts (exact); 16 d p and p in three.
 // Sums, maxima and the running softmax statistics are fp32.
@@ -248,7 +250,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) kv4_decode_kernel(const DecArg
     // ---- the tiles of this warp: tile0 + kWarps * i, i < n_it
     const int tile0 = j0 * kWarps + warp, n_tiles = (len + 15) >> 4;
     const int tile_end = min(n_tiles, j1 * kWarps);
-    const int n_it = tile0 < tile_end ? (tile_end - tile0 + kWarps - 1) / kWarps : 0;
+    int n_it = tile0 < tile_end ? (tile_end - tile0 + kWarps - 1) / kWarps : 0;
     const int tiles_per_page = a.page_size >> 4;
     const int32_t *table = a.table + (int64_t)seq * a.max_pages;
     // lane i holds the place of tile number `batch + i`, or -1
@@ -370,13 +372,17 @@ __global__ void __launch_bounds__(32 * kWarps, 2) kv4_decode_kernel(const DecArg
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[g][e][i] = 0.f;
     float m_run = -INFINITY, l_run = 0.f;  // of query head r; l over this thread's tokens
-    float room = kTop - 1.f;  // log2 that p may reach: kTop less that of the largest |d| met, 2 at least (16-bit types)
+    float room = kTop - 1.f;  // log2 that p may reach: kTop less that of the largest |d| met, 2 if that is less (16-bit types)
 
     for (int it = 0; it < n_it; ++it) {
       const int st = it % kStages;
       const uint32_t tile = ptx::smem_u32(ring + st * S::kTile);
       const bool came = ptx::mbar_wait_suspend(bar + st, (phase >> st) & 1u);
-      if (!__all_sync(0xffffffffu, came)) set_status(a.status, REDLITE_STATUS_TIMEOUT);
+      if (!__all_sync(0xffffffffu, came)) {  // no more tiles are asked for, those on their way are waited for
+        set_status(a.status, REDLITE_STATUS_TIMEOUT);
+        ptx::mbar_wait_suspend(bar + st, (phase >> st) & 1u);
+        n_it = min(n_it, it + kStages);
+      }
       phase ^= 1u << st;
       const int tok0 = 16 * (tile0 + kWarps * it);
       const int live = ((good >> st) & 1u) ? len - tok0 : 0;  // tokens of this tile that count
