@@ -29,11 +29,16 @@
 // per token in fp32.  Sums of log decays are fp64, held as two fp32 numbers
 // whose differences are rounded once.
 //
-// Measured (one B200): 16384 tokens, 16 / 32 heads of 128, bf16: 0.89 ms, of
-// which 0.19 ms preparation and 0.70 ms the chain, 2.7 us a chunk; eight packed
-// prompts of 3605 tokens, fp32: 0.27 ms.  The chain is bound by the latency of a
-// warp (four cycles an instruction, the tensor pipe busy 33%) and, in fp32, by
-// reads of shared memory (72%).  Other forms of it, for the same two calls:
+// Measured (one B200): 16384 tokens, 16 / 32 heads of 128, bf16: 0.84 ms, of
+// which 0.19 ms preparation and 0.66 ms the chain, 2.6 us a chunk; eight packed
+// prompts of 3605 tokens, fp32: 0.26 ms.  The chain is bound by the latency of a
+// warp (clocks of a chunk: 780 to split S, 870 K S, 570 beta V - K S split, 440
+// T times it, 340 D out, 1100 D split and S; the products alone 1300) and, in
+// fp32, by reads of shared memory (72%).  So operands are read and barriers
+// looked at one step ahead of their use (0.88 and 0.27 ms without).  Two warps
+// to a chain, each with one half of the keys, took 1.07 and 0.30 ms: the sums'
+// way through shared memory (900) and what both compute outweigh the halves.
+// Other forms of the chain, for the same two calls:
 // value columns as rows, 16 to a warp 0.88 ms (chain alone) and 0.22 ms, 16 to
 // two warps that share the keys 0.79 ms, columns 16 to a warp 1.09 and 0.21 ms,
 // and on tcgen05 (128 columns as lanes, operands through tensor memory, two
@@ -534,28 +539,35 @@ __device__ __forceinline__ void load_rows(uint32_t tile, int ks, int lane, uint3
   for (int t = 0; t < 4; ++t)
     ldsm4(tile + kq_off<DK>(16 * t + (lane & 15), 2 * ks + (lane >> 4)), a[t][0], a[t][1], a[t][2], a[t][3]);
 }
-// acc = L B: the lower triangle's blocks (two planes) times the B operands of 64 rows.
+// The lower triangle's blocks (two planes) of 16 columns.
 template <bool LO>
-__device__ __forceinline__ void triangle(float (&acc)[4][4], uint32_t planes, const uint32_t (&h)[4][2],
-                                         const uint32_t (&l)[4][2], int lane) {
-  float more[4][4];
-  zero(acc), zero(more);
+__device__ __forceinline__ void load_triangle(uint32_t planes, int ks, int lane, uint32_t (&p)[4][4], uint32_t (&q)[4][4]) {
 #pragma unroll
-  for (int ks = 0; ks < 4; ++ks) {
-    uint32_t p[4][4], q[4][4];
-#pragma unroll
-    for (int t = ks; t < 4; ++t) {
+  for (int t = 0; t < 4; ++t)
+    if (t >= ks) {
       const uint32_t off = planes + tp_off(16 * t + (lane & 15), 2 * ks + (lane >> 4));
       ldsm4(off, p[t][0], p[t][1], p[t][2], p[t][3]);
       if (LO) ldsm4(off + kPlane, q[t][0], q[t][1], q[t][2], q[t][3]);
     }
+}
+// acc = L B: the triangle times the B operands of 64 rows; p[0] and q[0] hold
+// its first 16 columns, the next ones are read while products run.
+template <bool LO>
+__device__ __forceinline__ void triangle(float (&acc)[4][4], uint32_t planes, const uint32_t (&h)[4][2],
+                                         const uint32_t (&l)[4][2], int lane, uint32_t (&p)[2][4][4],
+                                         uint32_t (&q)[2][4][4]) {
+  float more[4][4];
+  zero(acc), zero(more);
 #pragma unroll
-    for (int t = ks; t < 4; ++t) mma_f16(acc[t], p[t], h[ks][0], h[ks][1]);
+  for (int ks = 0; ks < 4; ++ks) {
+    if (ks < 3) load_triangle<LO>(planes, ks + 1, lane, p[(ks + 1) & 1], q[(ks + 1) & 1]);
+#pragma unroll
+    for (int t = ks; t < 4; ++t) mma_f16(acc[t], p[ks & 1][t], h[ks][0], h[ks][1]);
     if (LO) {
 #pragma unroll
-      for (int t = ks; t < 4; ++t) mma_f16(more[t], p[t], l[ks][0], l[ks][1]);
+      for (int t = ks; t < 4; ++t) mma_f16(more[t], p[ks & 1][t], l[ks][0], l[ks][1]);
 #pragma unroll
-      for (int t = ks; t < 4; ++t) mma_f16(more[t], q[t], h[ks][0], h[ks][1]);
+      for (int t = ks; t < 4; ++t) mma_f16(more[t], q[ks & 1][t], h[ks][0], h[ks][1]);
     }
   }
 #pragma unroll
@@ -577,11 +589,20 @@ template <>
 __device__ __forceinline__ void store2<__half>(__half *p, float x, float y) {
   *reinterpret_cast<uint32_t *>(p) = pack_f16(x, y);
 }
-__device__ __forceinline__ float2 load2(const float *p) { return *reinterpret_cast<const float2 *>(p); }
-__device__ __forceinline__ float2 load2(const __nv_bfloat16 *p) {
-  return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(p));
+// Two neighbours as they lie in memory.
+template <typename T>
+struct Pair {
+  typedef uint32_t type;
+};
+template <>
+struct Pair<float> {
+  typedef float2 type;
+};
+template <typename T>
+__device__ __forceinline__ float2 pair_f32(typename Pair<T>::type v) {
+  if constexpr (sizeof(T) == 4) return v;
+  else return make_float2(to_f32(reinterpret_cast<const T *>(&v)[0]), to_f32(reinterpret_cast<const T *>(&v)[1]));
 }
-__device__ __forceinline__ float2 load2(const __half *p) { return __half22float2(*reinterpret_cast<const __half2 *>(p)); }
 
 // Four chain warps, four output warps and one warp that issues the copies.
 // Block: (slice of 32 value columns, value head, sequence by falling length).
@@ -650,6 +671,18 @@ __global__ void __launch_bounds__(32 * (2 * kChains + 1), 1) delta_chain_kernel(
     if (!ok && lane == 0) set_status(a.status, REDLITE_STATUS_TIMEOUT);
     return ok;
   };
+  // the same for a phase that was looked at before (what came between hid the look)
+  auto test = [](uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+                 : "=r"(ok)
+                 : "r"(ptx::smem_u32(bar)), "r"(parity)
+                 : "memory");
+    return ok;
+  };
+  auto finish = [&](uint32_t came, uint64_t *bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, came) || wait(bar, parity);
+  };
   auto arrive = [&](uint64_t *bar) {
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(bar);
@@ -703,13 +736,15 @@ __global__ void __launch_bounds__(32 * (2 * kChains + 1), 1) delta_chain_kernel(
       const bool walk = ho.walk;
       arrive(bars->d_taken + me);
       if (!walk) {
+        uint32_t p[2][4][4], q[2][4][4];
+        load_triangle<kLo>(sP, 0, lane, p[0], q[0]);
         col_max(m0, m1);
         float i0, i1;
         const float s0 = scale_f16(m0, i0), s1 = scale_f16(m1, i1);
         uint32_t h[4][2], l[4][2];
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) split_tile(D[ks], s0, s1, h[ks], l[ks]);
-        triangle<kLo>(D, sP, h, l, lane);
+        triangle<kLo>(D, sP, h, l, lane, p, q);
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
@@ -763,6 +798,9 @@ __global__ void __launch_bounds__(32 * (2 * kChains + 1), 1) delta_chain_kernel(
     const uint32_t sK = ptx::smem_u32(smem + st * kStage), sT = sK + kq_bytes<NK, DK>();
     const float *f = reinterpret_cast<const float *>(smem + st * kStage + kq_bytes<NK, DK>() + kPlanes * kPlane);
     const T *vt = reinterpret_cast<const T *>(vbuf + (2 * me + (i & 1)) * Plan::kV);
+    const uint32_t full = test(bars->full + st, (i / kStages) & 1);
+    const uint32_t s_free = i == 0 || test(bars->s_taken + me, (i - 1) & 1);
+    const uint32_t d_free = i == 0 || test(bars->d_taken + me, (i - 1) & 1);
     // ---- the state in two parts
     float sm0 = 0.f, sm1 = 0.f;
 #pragma unroll
@@ -779,27 +817,37 @@ __global__ void __launch_bounds__(32 * (2 * kChains + 1), 1) delta_chain_kernel(
 #pragma unroll
       for (int ks = 0; ks < NT; ++ks) split_tile(S[ks], s0, s1, sh[ks], sl[ks]);
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncwarp();
     if (i + 1 < n_chunks) fetch_v(i + 1);
-    if (!wait(bars->full + st, (i / kStages) & 1)) break;
-    // ---- K S
+    if (!finish(full, bars->full + st, (i / kStages) & 1)) break;
+    // ---- K S (operands of every product are read one step ahead of it)
     float R[4][4], D[4][4];
     zero(R);
+    constexpr int kSteps = NK * NT;
+    uint32_t kr[2][4][4];
+    load_rows<DK>(sK, 0, lane, kr[0]);
+    // the rows' values and factors
+    typename Pair<T>::type vr[8];
+    float fb[8], fr[8];
 #pragma unroll
-    for (int ks = 0; ks < NT; ++ks) {
-      uint32_t k[4][4];
-      load_rows<DK>(sK, ks, lane, k);
+    for (int m = 0; m < 8; ++m) {
+      vr[m] = *reinterpret_cast<const typename Pair<T>::type *>(vt + (8 * m + r) * 8 + 2 * c);
+      fb[m] = f[fBeta * C + 8 * m + r], fr[m] = f[fR * C + 8 * m + r];
+    }
+#pragma unroll
+    for (int step = 0; step < kSteps; ++step) {
+      const int ks = step / NK;
+      if (step + 1 < kSteps) load_rows<DK>(sK + ((step + 1) % NK) * kTile, (step + 1) / NK, lane, kr[(step + 1) & 1]);
+      const auto &k = kr[step & 1];
 #pragma unroll
       for (int t = 0; t < 4; ++t) mma_f16(R[t], k[t], sh[ks][0], sh[ks][1]);
+      if (step % NK == 0)
 #pragma unroll
-      for (int t = 0; t < 4; ++t) mma_f16(R[t], k[t], sl[ks][0], sl[ks][1]);
-      if (NK == 2) {
-        load_rows<DK>(sK + kTile, ks, lane, k);
-#pragma unroll
-        for (int t = 0; t < 4; ++t) mma_f16(R[t], k[t], sh[ks][0], sh[ks][1]);
-      }
+        for (int t = 0; t < 4; ++t) mma_f16(R[t], k[t], sl[ks][0], sl[ks][1]);
     }
     // ---- the state's parts to the output warp, while the products run
-    if (i > 0 && !wait(bars->s_taken + me, (i - 1) & 1)) break;
+    if (i > 0 && !finish(s_free, bars->s_taken + me, (i - 1) & 1)) break;
 #pragma unroll
     for (int k2 = 0; k2 < NT / 2; ++k2) {
       ho.s[0][k2][lane] = make_uint4(sh[2 * k2][0], sh[2 * k2][1], sh[2 * k2 + 1][0], sh[2 * k2 + 1][1]);
@@ -807,20 +855,18 @@ __global__ void __launch_bounds__(32 * (2 * kChains + 1), 1) delta_chain_kernel(
     }
     if (r == 0) ho.scale[c] = make_float2(u0, u1);
     arrive(bars->s_ready + me);
-    if (i + 1 < n_chunks) asm volatile("cp.async.wait_group 1;" ::: "memory");
-    else asm volatile("cp.async.wait_group 0;" ::: "memory");
-    __syncwarp();
+    uint32_t tp[2][4][4], tq[2][4][4];
+    load_triangle<true>(sT, 0, lane, tp[0], tq[0]);
     // ---- beta V - beta exp(c) K S
     float m0 = 0.f, m1 = 0.f;
 #pragma unroll
     for (int t = 0; t < 4; ++t)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int j = 16 * t + 8 * e + r;
-        const float2 v = load2(vt + j * 8 + 2 * c);
-        const float fb = f[fBeta * C + j], fr = f[fR * C + j];
-        R[t][2 * e] = fmaf(fb, v.x, -fr * (R[t][2 * e] * u0));
-        R[t][2 * e + 1] = fmaf(fb, v.y, -fr * (R[t][2 * e + 1] * u1));
+        const int m = 2 * t + e;
+        const float2 v = pair_f32<T>(vr[m]);
+        R[t][2 * e] = fmaf(fb[m], v.x, -fr[m] * (R[t][2 * e] * u0));
+        R[t][2 * e + 1] = fmaf(fb[m], v.y, -fr[m] * (R[t][2 * e + 1] * u1));
         m0 = fmaxf(m0, fabsf(R[t][2 * e])), m1 = fmaxf(m1, fabsf(R[t][2 * e + 1]));
       }
     col_max(m0, m1);
@@ -832,23 +878,34 @@ __global__ void __launch_bounds__(32 * (2 * kChains + 1), 1) delta_chain_kernel(
       for (int ks = 0; ks < 4; ++ks) split_tile(R[ks], s0, s1, h[ks], l[ks]);
     }
     // ---- D = T R
-    triangle<true>(D, sT, h, l, lane);
     const float last = f[fLast * C];
+    float ft[8], fk[8];
+#pragma unroll
+    for (int m = 0; m < 8; ++m) ft[m] = f[fT * C + 8 * m + r], fk[m] = f[fK * C + 8 * m + r];
+    triangle<true>(D, sT, h, l, lane, tp, tq);
+    // K^T of 16 tokens
+    uint32_t kt[2][NT][4];
+    auto load_keys = [&](int step) {  // step: tokens 16 (step / NK) .., plane step % NK
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        ldsm4t(sK + (step % NK) * kTile +
+                   kq_off<DK>(16 * (step / NK) + (lane & 7) + ((lane >> 4) << 3), 2 * t + ((lane >> 3) & 1)),
+               kt[step & 1][t][0], kt[step & 1][t][1], kt[step & 1][t][2], kt[step & 1][t][3]);
+    };
+    load_keys(0);
     m0 = last * sm0 * sg0 * 0x1p-60f, m1 = last * sm1 * sg1 * 0x1p-60f;
-    if (i > 0 && !wait(bars->d_taken + me, (i - 1) & 1)) break;
+    if (i > 0 && !finish(d_free, bars->d_taken + me, (i - 1) & 1)) break;
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const float ft = f[fT * C + 16 * t + 8 * e + r];
-        D[t][2 * e] *= ft * i0, D[t][2 * e + 1] *= ft * i1;
+        D[t][2 * e] *= ft[2 * t + e] * i0, D[t][2 * e + 1] *= ft[2 * t + e] * i1;
         odd += (D[t][2 * e] - D[t][2 * e]) + (D[t][2 * e + 1] - D[t][2 * e + 1]);
       }
       ho.d[t][lane] = make_float4(D[t][0], D[t][1], D[t][2], D[t][3]);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const float fk = f[fK * C + 16 * t + 8 * e + r];
-        D[t][2 * e] *= fk, D[t][2 * e + 1] *= fk;
+        D[t][2 * e] *= fk[2 * t + e], D[t][2 * e + 1] *= fk[2 * t + e];
         m0 = fmaxf(m0, fabsf(D[t][2 * e])), m1 = fmaxf(m1, fabsf(D[t][2 * e + 1]));
       }
     }
@@ -866,20 +923,15 @@ __global__ void __launch_bounds__(32 * (2 * kChains + 1), 1) delta_chain_kernel(
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks) split_tile(D[ks], s0, s1, h[ks], l[ks]);
 #pragma unroll
-      for (int ks = 0; ks < 4; ++ks)
+      for (int step = 0; step < 4 * NK; ++step) {
+        const int ks = step / NK;
+        if (step + 1 < 4 * NK) load_keys(step + 1);
 #pragma unroll
-        for (int p = 0; p < NK; ++p) {
-          uint32_t k[NT][4];
+        for (int t = 0; t < NT; ++t) mma_f16(S[t], kt[step & 1][t], h[ks][0], h[ks][1]);
+        if (step % NK == 0)
 #pragma unroll
-          for (int t = 0; t < NT; ++t)
-            ldsm4t(sK + p * kTile + kq_off<DK>(16 * ks + (lane & 7) + ((lane >> 4) << 3), 2 * t + ((lane >> 3) & 1)),
-                   k[t][0], k[t][1], k[t][2], k[t][3]);
-#pragma unroll
-          for (int t = 0; t < NT; ++t) mma_f16(S[t], k[t], h[ks][0], h[ks][1]);
-          if (p == 0)
-#pragma unroll
-            for (int t = 0; t < NT; ++t) mma_f16(S[t], k[t], l[ks][0], l[ks][1]);
-        }
+          for (int t = 0; t < NT; ++t) mma_f16(S[t], kt[step & 1][t], l[ks][0], l[ks][1]);
+      }
     } else {
       // token by token from the state in front of the chunk
 #pragma unroll
@@ -911,7 +963,7 @@ __global__ void __launch_bounds__(32 * (2 * kChains + 1), 1) delta_chain_kernel(
             p0 = fmaf(k, S[t][2 * e], p0), p1 = fmaf(k, S[t][2 * e + 1], p1);
           }
         total(p0, p1);
-        const float2 v = load2(vt + j * 8 + 2 * c);
+        const float2 v = pair_f32<T>(*reinterpret_cast<const typename Pair<T>::type *>(vt + j * 8 + 2 * c));
         const float d0 = be * (v.x - al * nk * p0) * nk, d1 = be * (v.y - al * nk * p1) * nk;
         p0 = p1 = 0.f;
 #pragma unroll
