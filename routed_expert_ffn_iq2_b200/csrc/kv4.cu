@@ -154,10 +154,30 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(const Kv4Args a) {
   }
 }
 
-// d * code is exact; the code as the low bits of 2^23 + code.
-__device__ __forceinline__ void expand(uint32_t word, float d, float m, float (&x)[8]) {
+// Nibbles 0 .. N-1 of a word.  d * code is exact; the code as the low bits of
+// 2^23 + code.
+template <int N>
+__device__ __forceinline__ void expand(uint32_t word, float d, float m, float (&x)[N]) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = fmaf(d, __uint_as_float(((word >> (4 * i)) & 15u) | 0x4b000000u) - 8388608.f, m);
+  for (int i = 0; i < N; ++i) x[i] = fmaf(d, __uint_as_float(((word >> (4 * i)) & 15u) | 0x4b000000u) - 8388608.f, m);
+}
+// The values of word w of a row.  32-bit ones go out by pairs of threads, each
+// half of either's word, so that a store of the warp fills whole sectors.
+template <typename T, int D>
+__device__ __forceinline__ void put_words(T *row, int w, uint32_t word, float d, float m) {
+  if constexpr (sizeof(T) == 4) {
+    const int odd = w & 1;
+    const uint32_t other = __shfl_xor_sync(D == 256 ? 0xffffffffu : 0xffffu << (threadIdx.x & 16), word, 1);
+    float x[4], y[4];
+    expand((odd ? other : word) >> (16 * odd), d, m, x);
+    expand((odd ? word : other) >> (16 * odd), d, m, y);
+    float4 *p = reinterpret_cast<float4 *>(row + (w - odd) * 8) + odd;
+    p[0] = make_float4(x[0], x[1], x[2], x[3]), p[2] = make_float4(y[0], y[1], y[2], y[3]);
+  } else {
+    float x[8];
+    expand(word, d, m, x);
+    store8<T>(row + w * 8, x);
+  }
 }
 
 template <typename T, int D>
@@ -181,11 +201,8 @@ __global__ void __launch_bounds__(256) kv4_load_kernel(const Kv4Args a) {
     dv = __half2float(*reinterpret_cast<const __half *>(tile + kv4_v_step<D>(tok, g)));
     mv = __half2float(*reinterpret_cast<const __half *>(tile + kv4_v_min<D>(tok, g)));
   }
-  float x[8];
-  expand(kw, dk, mk, x);
-  store8<T>((T *)a.ko + row.token * a.k_stride + row.head * D + w * 8, x);
-  expand(vw, dv, mv, x);
-  store8<T>((T *)a.vo + row.token * a.v_stride + row.head * D + w * 8, x);
+  put_words<T, D>((T *)a.ko + row.token * a.k_stride + row.head * D, w, kw, dk, mk);
+  put_words<T, D>((T *)a.vo + row.token * a.v_stride + row.head * D, w, vw, dv, mv);
 }
 
 template <bool APPEND, typename T>
