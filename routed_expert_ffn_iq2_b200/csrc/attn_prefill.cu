@@ -22,8 +22,9 @@
 //               scores of step i + 1 are issued in front of the second product
 //               of step i, so the tensor cores work while the softmax does
 //   warp 2      tensor memory allocation
-//   warps 4 ..  softmax: thread = row.  Scores come out of tensor memory,
-//               probabilities go back over them in the inputs' type (that
+//   warps 4 ..  softmax: thread = row.  A step's scores come out of tensor memory
+//               in one read (in halves, read twice: 4.5 us more of the ragged
+//               batch below), probabilities go back over them in the inputs' type (that
 //               rounding, 2^-8 or 2^-11 of each p at most, is what the product's type
 //               asks for; l sums the unrounded p), half a row at a time: the
 //               second product starts on the first half of the keys
@@ -33,9 +34,10 @@
 //
 // Measured (one B200): 16384 tokens, 16 heads on 2 of 256, bf16: 1.62 to 1.73 ms,
 // 1.27 to 1.36 PFLOP/s (a long library product: 1.39); five ragged fp16 prompts,
-// 3957 tokens of 32 heads on 8 of 128: 73 us, 650 TFLOP/s; three of 43 tokens
+// 3957 tokens of 32 heads on 8 of 128: 68 to 72 us, 666 to 700 TFLOP/s; three of 43 tokens
 // together 8.1 us.  Tried without gain: two threads a row in the softmax,
-// polynomials for a part of the exponentials.
+// polynomials for a part of the exponentials, probabilities handed over in one
+// piece, tiles of all sequences by their keys instead of sequence by sequence.
 //
 // A zero probability times a NaN or an infinity in V is a NaN that a masked
 // key must not cause: a row whose result is not finite is computed again by
@@ -411,26 +413,19 @@ __global__ void __launch_bounds__(256, Shape<D>::kBlocks)
       __syncwarp();
       ptx::tc_fence_after();
       constexpr int kHalf = kKeys / 2;
-      uint32_t s[kHalf];  // one half's scores at a time
+      uint32_t s[kKeys];
       const int left = lim - i * kKeys;  // keys of this tile that the row sees
-      const bool edge = __any_sync(0xffffffffu, left < kKeys);
-      auto load = [&](int h) {
 #pragma unroll
-        for (int j = 0; j < kHalf; j += 32) tmem_ld32(t_s + kHalf * h + j, s + j);
-        ptx::tmem_wait_ld();
-        if (edge) {
+      for (int j = 0; j < kKeys; j += 32) tmem_ld32(t_s + j, s + j);
+      ptx::tmem_wait_ld();
+      if (__any_sync(0xffffffffu, left < kKeys)) {
 #pragma unroll
-          for (int j = 0; j < kHalf; ++j) s[j] = kHalf * h + j < left ? s[j] : 0xff800000u;
-        }
-      };
+        for (int j = 0; j < kKeys; ++j) s[j] = j < left ? s[j] : 0xff800000u;
+      }
       float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int h = 1; h >= 0; --h) {
-        load(h);
-#pragma unroll
-        for (int j = 0; j < kHalf; j += 2)
-          mx[(j >> 1) & 3] = fmaxf(fmaxf(mx[(j >> 1) & 3], __uint_as_float(s[j])), __uint_as_float(s[j + 1]));
-      }
+      for (int j = 0; j < kKeys; j += 2)
+        mx[(j >> 1) & 3] = fmaxf(fmaxf(mx[(j >> 1) & 3], __uint_as_float(s[j])), __uint_as_float(s[j + 1]));
       const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
       if (__any_sync(0xffffffffu, top > m + kLazy || (m == -INFINITY && top > -INFINITY))) {
         const float mn = fmaxf(m, top);
@@ -458,16 +453,15 @@ __global__ void __launch_bounds__(256, Shape<D>::kBlocks)
       uint64_t sum[2] = {0, 0};
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        if (h) load(h);
         uint32_t p[kHalf / 2];
 #pragma unroll
         for (int j = 0; j < kHalf / 2; ++j) {
-          const float2 z = unpair(fma2(pair(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])), scale2, neg2));
+          const float2 z = unpair(fma2(pair(__uint_as_float(s[kHalf * h + 2 * j]), __uint_as_float(s[kHalf * h + 2 * j + 1])), scale2, neg2));
           const float x = ex2(z.x), y = ex2(z.y);
           sum[j & 1] = add2(sum[j & 1], pair(x, y));
           p[j] = kBf ? pack_bf16(x, y) : pack_f16(x, y);
         }
-        // over scores that are in registers or done with
+        // over scores that are in registers
 #pragma unroll
         for (int j = 0; j < kHalf / 2; j += 16) tmem_st16(t_s + kHalf / 2 * h + j, p + j);
         ptx::tmem_wait_st();
