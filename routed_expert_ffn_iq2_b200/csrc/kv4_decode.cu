@@ -24,6 +24,9 @@
 //               leaves fp16:
 //               p <= 2^15 / max(1, |d|) for the largest |d| met so far.
 //   fp32        the query in three bf16 parts (exact); 16 d p and p in three.
+//               Codes are centred in the scores too: q . K_t = sum_g 16 d_tg (q_g
+//               . (code - 8) / 16) + (m_tg + 8 d_tg) sum(q_g), so that no sum is
+//               much larger than what it stands for.
 // Sums, maxima and the running softmax statistics are fp32.
 //
 // Split: the units of all sequences (128 tokens of one key/value head and up
@@ -425,7 +428,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) kv4_decode_kernel(const DecArg
             s[2] = fmaf(db, x[2], s[2]), s[3] = fmaf(db, x[3], s[3]);
           } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) A0[i] = code_pair(wa[gg], i), A1[i] = code_pair(wb[gg], i);
+            for (int i = 0; i < 4; ++i) A0[i] = centre(code_pair(wa[gg], i)), A1[i] = centre(code_pair(wb[gg], i));
 #pragma unroll
             for (int p = 0; p < NS; ++p) {
               const uint4 b = qf[(p * NG + g) * 32 + lane];
@@ -434,7 +437,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) kv4_decode_kernel(const DecArg
             }
             const float2 sum = *reinterpret_cast<const float2 *>(qs + g * 8 + 2 * c);
             const float da = 16.f * h_lo(ka[gg]), db = 16.f * h_lo(kb[gg]);
-            const float ma = h_hi(ka[gg]) - da, mb = h_hi(kb[gg]) - db;
+            const float ma = fmaf(0.5f, da, h_hi(ka[gg])), mb = fmaf(0.5f, db, h_hi(kb[gg]));
             s[0] = fmaf(da, x[0], fmaf(ma, sum.x, s[0]));
             s[1] = fmaf(da, x[1], fmaf(ma, sum.y, s[1]));
             s[2] = fmaf(db, x[2], fmaf(mb, sum.x, s[2]));
