@@ -34,7 +34,7 @@
 // prompts of 3605 tokens, fp32: 0.26 ms.  The chain is bound by the latency of a
 // warp (clocks of a chunk: 780 to split S, 870 K S, 570 beta V - K S split, 440
 // T times it, 340 D out, 1100 D split and S; the products alone 1300) and, in
-// fp32, by reads of shared memory (72%).  So operands are read and barriers
+// fp32, by reads of shared memory (76%).  So operands are read and barriers
 // looked at one step ahead of their use (0.88 and 0.27 ms without).  Two warps
 // to a chain, each with one half of the keys, took 1.07 and 0.30 ms: the sums'
 // way through shared memory (900) and what both compute outweigh the halves.
