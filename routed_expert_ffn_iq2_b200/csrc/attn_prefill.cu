@@ -40,7 +40,7 @@
 // piece, tiles of all sequences by their keys instead of sequence by sequence.
 //
 // A zero probability times a NaN or an infinity in V is a NaN that a masked
-// key must not cause: a row whose result is not finite is computed again by
+// key must not cause, and a sum over values past 10^36 may leave fp32: a row whose result is not finite is computed again by
 // its warp from the keys it sees alone.
 #include <cuda.h>
 
@@ -187,7 +187,8 @@ __device__ __forceinline__ bool wait(Bars<D> *b, uint64_t *bar, uint32_t parity,
   return false;
 }
 
-// One row by one warp, from the keys it sees alone, fp32.
+// One row by one warp, from the keys it sees alone, fp32; o is the mean so far,
+// so that values near the end of bf16's range do not leave fp32's in a sum.
 template <typename T, int D>
 __device__ __noinline__ void row_again(const AttnArgs &a, int64_t q_row, int head, int64_t k_row0, int lim) {
   constexpr int E = D / 32;
@@ -209,15 +210,16 @@ __device__ __noinline__ void row_again(const AttnArgs &a, int64_t q_row, int hea
     s *= a.scale_log2;
     const float mn = s > m ? s : m;  // a NaN leaves m and makes p a NaN
     const float f = m == -INFINITY ? 0.f : ex2(m - mn), p = s == -INFINITY ? 0.f : ex2(s - mn);
-    l = l * f + p;
+    const float old = l * f;
+    l = old + p;
+    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l), w0 = old * inv, w1 = p * inv;
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = o[e] * f + p * to_f32(v[lane + 32 * e]);
+    for (int e = 0; e < E; ++e) o[e] = o[e] * w0 + w1 * to_f32(v[lane + 32 * e]);
     m = mn;
   }
-  const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
 #pragma unroll
   for (int e = 0; e < E; ++e)
-    ((T *)a.out)[q_row * a.out_stride + (int64_t)head * D + lane + 32 * e] = from_f32<T>(o[e] * inv);
+    ((T *)a.out)[q_row * a.out_stride + (int64_t)head * D + lane + 32 * e] = from_f32<T>(o[e]);
 }
 
 template <typename T, int D>

@@ -193,6 +193,20 @@ def test_attention_over_many_sequences(P, t, D, n):
 
 
 @gpu
+@pytest.mark.parametrize("t,top", [(torch.bfloat16, 3e38), (torch.float16, 6e4)])
+@pytest.mark.parametrize("D", [128, 256])
+def test_attention_values_near_the_end_of_the_range(P, t, top, D):
+    """Values whose unnormalised sums leave fp32 (bf16): their mean does not."""
+    rng = np.random.default_rng(D)
+    q, k, v = TA._inputs(rng, t, 150, 150, 4, 2, D)
+    v[:, 0] = top                                             # all alike
+    v[:, 1] = (top * torch.sign(v[:, 1].float())).to(t)       # of either sign
+    out = torch.empty_like(q)
+    assert P.redlite_attn_prefill(q, k, v, R.cu([150]), R.cu([150]), out, 0.05) == P.REDLITE_OK
+    TA._check(out, *TA._reference(TA._host(q), TA._host(k), TA._host(v), [150], [150], 0.05, t))
+
+
+@gpu
 def test_attention_without_any_key(P):
     """Every sequence without keys, and no key rows at all: zeros."""
     q = torch.randn(7, 4, 128, device="cuda").bfloat16()
