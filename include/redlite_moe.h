@@ -424,7 +424,9 @@ int redlite_kv4_load(int32_t dtype, const void *cache, int32_t n_kv_heads, int32
  * to fp16 (relative to p d code that is 2^-10 at most, of either sign).
  * lens: device int32 [n_seqs]; a sequence of length 0 gives zeros, and so does one whose length
  * is negative or beyond max_pages * page_size (reported); tokens on a page
- * that is not in the cache are left out (reported).
+ * that is not in the cache are left out (reported).  A NaN in a query, or among the
+ * keys that count, gives NaN for the heads that meet it; one among the values
+ * gives NaN in its group.
  *   q, out   device [n_seqs rows, n_heads * head_dim]
  *   workspace device, 16-byte aligned, redlite_kv4_decode_workspace_bytes()
  * The result does not depend on the order in which blocks run. */

@@ -190,6 +190,11 @@ __device__ __forceinline__ void ldsm2(uint32_t addr, uint32_t &a, uint32_t &b) {
 __device__ __forceinline__ float h_lo(uint32_t v) { return __half2float(__ushort_as_half((uint16_t)v)); }
 __device__ __forceinline__ float h_hi(uint32_t v) { return __half2float(__ushort_as_half((uint16_t)(v >> 16))); }
 
+// Whether a partial result {m, l} holds any token.  Comparisons pass over a
+// NaN, so tokens whose scores are all NaN leave m at -infinity; their sum is
+// NaN then, and has to reach the result.
+__device__ __forceinline__ bool counts(float2 ml) { return ml.x > -INFINITY || ml.y != 0.f; }
+
 template <typename T, int D>
 __global__ void __launch_bounds__(32 * kWarps, 2) kv4_decode_kernel(const DecArgs a) {
   using S = DecSmem<D>;
@@ -673,7 +678,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) kv4_decode_kernel(const DecArg
         const float f = ex2(v.x - base);
         const float4 x =
             *reinterpret_cast<const float4 *>(ring_all + w * kStages * S::kTile + (size_t)(h * D + 4 * d4) * 4);
-        if (v.x > -INFINITY) {
+        if (counts(v)) {
           l = fmaf(f, v.y, l);
           o.x = fmaf(f, x.x, o.x), o.y = fmaf(f, x.y, o.y), o.z = fmaf(f, x.z, o.z), o.w = fmaf(f, x.w, o.w);
         }
@@ -754,7 +759,7 @@ __global__ void __launch_bounds__(256) kv4_join_kernel(const DecArgs a) {
     const float *p = part(i);
     const float2 v = *reinterpret_cast<const float2 *>(p + 8 * D + 2 * h);
     const float4 x = *(reinterpret_cast<const float4 *>(p + h * D) + d4);
-    if (v.x > -INFINITY) {
+    if (counts(v)) {
       const float f = ex2(v.x - base);
       l = fmaf(f, v.y, l);
       o.x = fmaf(f, x.x, o.x), o.y = fmaf(f, x.y, o.y), o.z = fmaf(f, x.z, o.z), o.w = fmaf(f, x.w, o.w);
