@@ -78,7 +78,7 @@ struct DecArgs {
 __device__ __forceinline__ int seq_units(const DecArgs &a, int s) {
   const int n = __ldg(a.lens + s);
   if (n <= 0 || (int64_t)n > (int64_t)a.max_pages * a.page_size) return 0;
-  return (n + kUnit - 1) / kUnit + kEntry;
+  return (n - 1) / kUnit + 1 + kEntry;  // (a sum with n may leave 32 bits)
 }
 
 // Sum of the units of all sequences (of one head block), and where unit u of
@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) kv4_decode_kernel(const DecArg
     const int head0 = kvh * a.ratio + hb * 8, n_h = min(8, a.ratio - hb * 8);
 
     // ---- the tiles of this warp: tile0 + kWarps * i, i < n_it
-    const int tile0 = j0 * kWarps + warp, n_tiles = (len + 15) >> 4;
+    const int tile0 = j0 * kWarps + warp, n_tiles = ((len - 1) >> 4) + 1;
     const int tile_end = min(n_tiles, j1 * kWarps);
     int n_it = tile0 < tile_end ? (tile_end - tile0 + kWarps - 1) / kWarps : 0;
     const int tiles_per_page = a.page_size >> 4;
