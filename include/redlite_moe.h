@@ -421,7 +421,8 @@ int redlite_kv4_load(int32_t dtype, const void *cache, int32_t n_kv_heads, int32
  *   out[s, h] = sum_{t < lens[s]} softmax_t(scale * q[s, h] . K[t, kh]) V[t, kh]
  * K, V the values the cache stands for, never rounded themselves; with 16-bit
  * activations a probability and its product with a group's step d are rounded
- * to fp16 (relative to p d code that is 2^-10 at most, of either sign).
+ * to fp16: of p d (code - 8), 2^-10 at most, or 2^-22 of the largest p times
+ * the head's largest |d| times |code - 8| where that is more, of either sign.
  * lens: device int32 [n_seqs]; a sequence of length 0 gives zeros, and so does one whose length
  * is negative or beyond max_pages * page_size (reported); tokens on a page
  * that is not in the cache are left out (reported).  A NaN in a query, or among the

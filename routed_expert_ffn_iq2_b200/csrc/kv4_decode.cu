@@ -22,7 +22,11 @@
 //               over p m and the softmax's own sum keep p whole).  The
 //               reference of the softmax is kept so that neither p nor p d
 //               leaves fp16:
-//               p <= 2^15 / max(1, |d|) for the largest |d| met so far.
+//               p <= 2^15 / max(1, |d|) for the largest |d| met so far.  Small steps
+//               count as 2^lift times themselves, so that p d stays above fp16's
+//               subnormal numbers: what falls below them all the same is off by
+//               2^-22 of the largest p d at most (without: by 2^-25 of a p of 2^6 to
+//               2^14, 2^-9 of the output where values are 1e-6)
 //   fp32        the query in three bf16 parts (exact); 16 d p and p in three.
 //               Codes are centred in the scores too: q . K_t = sum_g 16 d_tg (q_g
 //               . (code - 8) / 16) + (m_tg + 8 d_tg) sum(q_g), so that no sum is
@@ -58,6 +62,10 @@ constexpr int kUnit = 16 * kWarps;  // tokens of a unit
 constexpr int kEntry = 4;
 constexpr float kLazy = 8.f;        // log2 by which scores may pass the reference before sums are rescaled
 constexpr float kTop = 15.f;        // log2 that p, and p |d|, stay below in fp16
+// Steps are lifted where the largest of a run's first tile is below
+// 2^(kLiftBelow - 1) (values of 2^-6 and less); at 2^-9 a p d of the largest p
+// (2^6 at least) is 2^11 above fp16's smallest normal number.
+constexpr int kLiftBelow = -8;
 
 struct DecArgs {
   const void *q;
@@ -380,6 +388,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) kv4_decode_kernel(const DecArg
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[g][e][i] = 0.f;
     float m_run = -INFINITY, l_run = 0.f;  // of query head r; l over this thread's tokens
+    int lift = 0;             // steps count as 2^lift times themselves in `acc`
     float room = kTop - 1.f;  // log2 that p may reach: kTop less that of the largest |d| met, 2 if that is less (16-bit types)
 
     for (int it = 0; it < n_it; ++it) {
@@ -495,7 +504,9 @@ __global__ void __launch_bounds__(32 * kWarps, 2) kv4_decode_kernel(const DecArg
         for (int i = 0; i < 4; ++i)
 #pragma unroll
           for (int g = 0; g < NG / 2; ++g) any |= dw[i][g];
-        if (__any_sync(0xffffffffu, any & 0x40004000u)) {  // a step of 2 or more (`room` starts one below for the rest)
+        // a step of 2 or more (`room` starts one below for the rest); the first
+        // tile, which says whether steps are lifted, and every one while they are
+        if (it == 0 || lift || __any_sync(0xffffffffu, any & 0x40004000u)) {
           __half2 big = __habs2(as_h2(dw[0][0]));
 #pragma unroll
           for (int i = 0; i < 4; ++i)
@@ -503,9 +514,28 @@ __global__ void __launch_bounds__(32 * kWarps, 2) kv4_decode_kernel(const DecArg
             for (int g = 0; g < NG / 2; ++g) big = __hmax2(big, __habs2(as_h2(dw[i][g])));
           big = __hmax2(big, as_h2(__shfl_xor_sync(0xffffffffu, as_u32(big), 1)));
           big = __hmax2(big, as_h2(__shfl_xor_sync(0xffffffffu, as_u32(big), 2)));
-          // 2^n > top for n = exponent + 1; at most 16
+          // 2^n > top >= 2^(n - 1); at most 16
           const float top = fmaxf(__low2float(big), __high2float(big));
-          room = fminf(room, kTop - (float)min(16, max(0, (int)(__float_as_uint(top) >> 23) - 126)));
+          const int n = (int)(__float_as_uint(top) >> 23) - 126;
+          room = fminf(room, kTop - (float)min(16, max(0, n)));
+          const int to = it == 0 ? (n < kLiftBelow ? min(1 - n, 15) : 0) : min(lift, max(0, 1 - n));
+          if (to != lift && it > 0) {
+            const float f = __int_as_float((127 + to - lift) << 23);
+#pragma unroll
+            for (int g = 0; g < NG; ++g)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[g][e][i] *= f;
+          }
+          lift = to;
+        }
+        if (lift) {
+          const __half2 f = as_h2((uint32_t)(15 + lift) * 0x04000400u);  // 2^lift
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int g = 0; g < NG / 2; ++g) dw[i][g] = as_u32(__hmul2(as_h2(dw[i][g]), f));
         }
       }
       // rescale only when a score passes the reference by 2^8 (16-bit types: by
@@ -656,10 +686,12 @@ __global__ void __launch_bounds__(32 * kWarps, 2) kv4_decode_kernel(const DecArg
         g1 = fmaf(8.f, __shfl_sync(0xffffffffu, accm[1], (g + 4) * 4 + c), g1);
       }
       float *h0 = mine + (2 * c) * D + 32 * g + 4 * r, *h1 = h0 + D;
-      *reinterpret_cast<float4 *>(h0) =
-          make_float4(acc[g][0][0] + g0, acc[g][0][2] + g0, acc[g][1][0] + g0, acc[g][1][2] + g0);
-      *reinterpret_cast<float4 *>(h1) =
-          make_float4(acc[g][0][1] + g1, acc[g][0][3] + g1, acc[g][1][1] + g1, acc[g][1][3] + g1);
+      const float un = kHalf ? __int_as_float((127 - lift) << 23) : 1.f;
+      auto sum = [&](float x, float y) { return kHalf ? fmaf(x, un, y) : x + y; };
+      *reinterpret_cast<float4 *>(h0) = make_float4(sum(acc[g][0][0], g0), sum(acc[g][0][2], g0), sum(acc[g][1][0], g0),
+                                                    sum(acc[g][1][2], g0));
+      *reinterpret_cast<float4 *>(h1) = make_float4(sum(acc[g][0][1], g1), sum(acc[g][0][3], g1), sum(acc[g][1][1], g1),
+                                                    sum(acc[g][1][3], g1));
     }
     __syncthreads();
     const bool whole = j0 == 0 && j1 == n_units - kEntry;
