@@ -893,7 +893,9 @@ __global__ void __launch_bounds__(32 * (2 * kChains + 1), 1) delta_chain_kernel(
                kt[step & 1][t][0], kt[step & 1][t][1], kt[step & 1][t][2], kt[step & 1][t][3]);
     };
     load_keys(0);
-    m0 = last * sm0 * sg0 * 0x1p-60f, m1 = last * sm1 * sg1 * 0x1p-60f;
+    // (at least 2^-108 of the old scale, so that f0 below stays in fp32 also
+    // where nothing is left of the state)
+    m0 = last * sg0 * fmaxf(sm0 * 0x1p-60f, 0x1p-108f), m1 = last * sg1 * fmaxf(sm1 * 0x1p-60f, 0x1p-108f);
     if (i > 0 && !finish(d_free, bars->d_taken + me, (i - 1) & 1)) break;
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
