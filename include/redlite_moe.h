@@ -404,7 +404,9 @@ size_t redlite_kv4_page_bytes(int32_t n_kv_heads, int32_t head_dim, int32_t page
 
 /* Store the new tokens' keys and values: row cu[s] + i of k and v becomes
  * token start[s] + i of sequence s.  start: device int32 [n_seqs].  What a
- * place holds after a call that maps two rows to it is open. */
+ * place holds after a call that maps two rows to it is open.  Offsets that do
+ * not ascend within 0 .. n_tokens are reported (here and by the reverse);
+ * which sequence the rows around them count for is open then. */
 int redlite_kv4_append(int32_t dtype, const void *k, const void *v, int64_t k_stride, int64_t v_stride,
                        const int32_t *cu_tokens, const int32_t *start, int32_t n_seqs, int32_t n_tokens,
                        int32_t n_kv_heads, int32_t head_dim, int32_t page_size, const int32_t *block_table,

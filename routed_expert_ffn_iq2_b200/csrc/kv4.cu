@@ -72,6 +72,16 @@ __device__ __forceinline__ uint8_t *row_tile(const Kv4Args &a, int64_t row, int 
   return a.cache + kv4_tile_offset<D>(page, a.n_heads, head, a.page_size, in_page >> 4);
 }
 
+// The first block reports sequences whose offsets do not ascend within the
+// rows (what rows they leave to others is found row by row).
+__device__ __forceinline__ void check_offsets(const Kv4Args &a) {
+  if (blockIdx.x | blockIdx.y) return;
+  for (int s = threadIdx.x; s < a.n_seqs; s += blockDim.x) {
+    const int b = __ldg(a.cu + s), e = __ldg(a.cu + s + 1);
+    if (b < 0 || e < b || e > a.n_tokens) set_status(a.status, REDLITE_STATUS_BAD_LENGTH);
+  }
+}
+
 // Codes of eight values and the step and minimum of their group of 32 (four
 // threads).  Step and minimum are stored in 16 bits (11 significant ones, a
 // quarter of a bit per value); the codes are chosen for the stored pair.
@@ -127,6 +137,7 @@ __device__ __forceinline__ uint32_t quantise(const float (&x)[8], __half &dh, __
 template <typename T, int D>
 __global__ void __launch_bounds__(256) kv4_append_kernel(const Kv4Args a) {
   after_predecessor();
+  check_offsets(a);
   const Rows<D> row(a);
   const int w = threadIdx.x % Rows<D>::kWords, g = w >> 2, c = w & 3;
   // a row's threads share these conditions, and the shuffles stay inside
@@ -184,6 +195,7 @@ __device__ __forceinline__ void put_words(T *row, int w, uint32_t word, float d,
 template <typename T, int D>
 __global__ void __launch_bounds__(256) kv4_load_kernel(const Kv4Args a) {
   after_predecessor();
+  check_offsets(a);
   const Rows<D> row(a);
   if (!row.live) return;
   const int w = threadIdx.x % Rows<D>::kWords, g = w >> 2, c = w & 3;
