@@ -381,6 +381,8 @@ int redlite_proj_gemv(int32_t qtype, const void *W, int64_t rows, int64_t k, con
  *   k, v        device [n_k rows, n_kv_heads * head_dim]
  *   cu_q, cu_k  device [n_seqs + 1] each; a sequence whose offsets do not
  *               ascend within the rows is reported, its outputs not written
+ *               (where cu_q falls, what the others give is open; nothing out
+ *               of range is read or written)
  *   head_dim    128 or 256;  scale > 0, finite
  * Probabilities are rounded to dtype in front of the second product. */
 int redlite_attn_prefill(int32_t dtype, const void *q, int64_t q_stride, const void *k, int64_t k_stride,
@@ -396,8 +398,9 @@ int redlite_attn_prefill(int32_t dtype, const void *q, int64_t q_stride, const v
  * not read; a page may serve several sequences as long as none writes it).
  * Values are kept in groups of 32 along the head:
  *   m = fp16(min), d = fp16((max - m) / 15) (difference and quotient in
- *   fp32), code = the nearest of 0..15 to (x - m) / d (ties to even, 0 if
- *   d = 0); the cache stands for m + d * code.
+ *   fp32), code = the nearest of 0..15 to (x - m) / d (ties to even; 0 unless
+ *   d > 0: values that fp16 does not tell apart may round up to an m past
+ *   their max, and d is stored as it comes); the cache stands for m + d * code.
  * Inputs are clamped to +-65504; a group that holds a NaN or an infinity
  * reads back as NaN.  head_dim 128 or 256. */
 size_t redlite_kv4_page_bytes(int32_t n_kv_heads, int32_t head_dim, int32_t page_size);

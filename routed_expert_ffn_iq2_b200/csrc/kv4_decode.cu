@@ -17,16 +17,17 @@
 // (that needs no shift of its own), the query's element is 16 times as large.
 // Two forms of the rest:
 //   16-bit activations  a head's query scaled by a power of two into one fp16
-//               part (exact); p and p d are rounded to fp16 (2^-10 of each
-//               term's p d (code - 8) in all at most, of either sign; the sum
-//               over p m and the softmax's own sum keep p whole).  The
-//               reference of the softmax is kept so that neither p nor p d
-//               leaves fp16:
-//               p <= 2^15 / max(1, |d|) for the largest |d| met so far.  Small steps
-//               count as 2^lift times themselves, so that p d stays above fp16's
-//               subnormal numbers: what falls below them all the same is off by
-//               2^-22 of the largest p d at most (without: by 2^-25 of a p of 2^6 to
-//               2^14, 2^-9 of the output where values are 1e-6)
+//               part (exact for elements down to 2^-19 of the head's largest,
+//               2^-22 for bf16; below, off by 2^-30 of that at most); p and p d
+//               are rounded to fp16 (2^-10 of each term's p d (code - 8) in all
+//               at most, of either sign; the sum over p m and the softmax's own
+//               sum keep p whole).  The reference of the softmax is kept so that
+//               neither p nor p d leaves fp16:
+//               p <= 2^15 / max(1, |d|) for the largest |d| met so far.  Small
+//               steps count as 2^lift times themselves, so that p d stays above
+//               fp16's subnormal numbers: what falls below them all the same is
+//               off by 2^-22 of the largest p d at most (without: by 2^-25 of a p
+//               of 2^6 to 2^14, 2^-9 of the output where values are 1e-6)
 //   fp32        the query in three bf16 parts (exact); 16 d p and p in three.
 //               Codes are centred in the scores too: q . K_t = sum_g 16 d_tg (q_g
 //               . (code - 8) / 16) + (m_tg + 8 d_tg) sum(q_g), so that no sum is
