@@ -311,10 +311,16 @@ _marshal_mod = None
 
 
 def _marshal():
-    """The native argument marshaller (raises if it is not built)."""
+    """The native argument marshaller (raises if it is not built, or built for another Python or torch)."""
     global _marshal_mod
     if _marshal_mod is None:
         lib()
+        from . import build
+
+        if not os.path.exists(build.MARSHAL):
+            raise RuntimeError(f"{build.MARSHAL} is not built; run build()")
+        if not build.marshal_abi_matches():
+            raise RuntimeError(f"{build.MARSHAL} was built against another Python or torch; run build()")
         from . import _marshal as mod  # beside libredlite_moe.so, built with it
 
         _marshal_mod = mod

@@ -8,6 +8,7 @@ import os
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -15,6 +16,7 @@ CSRC = os.path.join(PKG, "csrc")
 OBJ = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libredlite_moe.so")
 MARSHAL = os.path.join(PKG, "_marshal.so")
+MARSHAL_ABI = os.path.join(OBJ, "_marshal.abi")  # what the marshaller was built against
 
 CXX = os.environ.get("CXX", "g++")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
@@ -41,13 +43,34 @@ def up_to_date() -> bool:
     return _newer(LIB, _deps())
 
 
+def marshal_abi() -> str:
+    """The Python and torch that _marshal.so has to be built against: its file name does not tell."""
+    import torch
+
+    return " ".join([sysconfig.get_config_var("EXT_SUFFIX"), torch.__version__,
+                     f"cxx11abi={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"])
+
+
+def marshal_abi_matches() -> bool:
+    """Whether _marshal.so was built against this Python and torch (and its last build went through)."""
+    try:
+        with open(MARSHAL_ABI) as f:
+            return f.read() == marshal_abi()
+    except OSError:
+        return False
+
+
 def build_marshal(force: bool = False) -> str:
     """_marshal.so against torch's headers and libredlite_moe.so (found beside it)."""
     src = os.path.join(CSRC, "marshal.cpp")
-    if not force and _newer(MARSHAL, [src, os.path.join(ROOT, "include", "redlite_moe.h")]):
+    if (not force and _newer(MARSHAL, [src, os.path.join(ROOT, "include", "redlite_moe.h")])
+            and marshal_abi_matches()):
         return MARSHAL
     import torch
 
+    os.makedirs(OBJ, exist_ok=True)
+    if os.path.exists(MARSHAL_ABI):
+        os.remove(MARSHAL_ABI)  # until the build below has gone through
     t = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(NVCC))
     inc = [os.path.join(ROOT, "include"), os.path.join(t, "include"),
@@ -62,12 +85,23 @@ def build_marshal(force: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError("marshal.cpp failed:\n" + r.stdout.decode(errors="replace"))
     os.replace(tmp, MARSHAL)
+    with open(MARSHAL_ABI, "w") as f:
+        f.write(marshal_abi())
     return MARSHAL
+
+
+def _try_marshal(force: bool = False) -> None:
+    """The library stands without the marshaller: what cannot be compiled against this torch costs the token mixers'
+    Python calls alone (they raise), not the C ABI nor the routed layer."""
+    try:
+        build_marshal(force)
+    except (OSError, RuntimeError) as e:
+        warnings.warn(f"the token mixers' Python calls are not available: {e}")
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
     if not force and up_to_date():
-        build_marshal()
+        _try_marshal()
         return LIB
     os.makedirs(OBJ, exist_ok=True)
     procs, objs = [], []
@@ -91,7 +125,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     subprocess.check_call([NVCC, "-gencode", "arch=compute_100a,code=sm_100a", "-shared", "--cudart", "static",
                            "-o", tmp, *objs])
     os.replace(tmp, LIB)
-    build_marshal(force)
+    _try_marshal(force)
     return LIB
 
 
