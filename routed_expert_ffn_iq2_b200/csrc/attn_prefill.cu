@@ -21,7 +21,8 @@
 //   warp 1      issues the products.  Two score buffers are used in turn: the
 //               scores of step i + 1 are issued in front of the second product
 //               of step i, so the tensor cores work while the softmax does
-//   warp 2      tensor memory allocation
+//   warps 2, 3  zeros over the last values that no row sees; warp 2 allocates the
+//               tensor memory too
 //   warps 4 ..  softmax: thread = row.  A step's scores come out of tensor memory
 //               in one read (in halves, read twice: 4.5 us more of the ragged
 //               batch below), probabilities go back over them in the inputs' type (that
@@ -40,8 +41,13 @@
 // piece, tiles of all sequences by their keys instead of sequence by sequence.
 //
 // A zero probability times a NaN or an infinity in V is a NaN that a masked
-// key must not cause, and a sum over values past 10^36 may leave fp32: a row whose result is not finite is computed again by
-// its warp from the keys it sees alone.
+// key must not cause.  Of the keys that no row of a block sees (behind a
+// sequence, or later tokens) the last product leaves out all it can, and the
+// values of the up to 15 others are set to zero in shared memory (with NaN
+// behind 8189 keys, 512 queries of 16 heads took 142 ms without, as every row
+// of the last tile was computed again).  Among a block's own tokens,
+// and where a sum over values past 10^36 leaves fp32, the columns of a row that
+// are not finite are computed again by its warp from the keys it sees alone.
 #include <cuda.h>
 
 #include <type_traits>
@@ -79,7 +85,7 @@ struct Shape {
 
 template <int D>
 struct Bars {
-  uint64_t q_full, full[Shape<D>::kRing], empty[Shape<D>::kRing], s_full[2], p_half[2], p_full[2], o_full, done;
+  uint64_t q_full, full[Shape<D>::kRing], empty[Shape<D>::kRing], s_full[2], p_half[2], p_full[2], o_full, done, tail;
   uint32_t tmem;
   int dead;
 };
@@ -187,39 +193,74 @@ __device__ __forceinline__ bool wait(Bars<D> *b, uint64_t *bar, uint32_t parity,
   return false;
 }
 
-// One row by one warp, from the keys it sees alone, fp32; o is the mean so far,
-// so that values near the end of bf16's range do not leave fp32's in a sum.
+// The columns of one row that are not finite, by one warp, from the keys the
+// row sees alone, fp32; eight keys at a time.  o is the mean so far, so that
+// values near the end of bf16's range do not leave fp32's in a sum.  The walk
+// ends where a NaN has reached every such column (nothing takes it away).
 template <typename T, int D>
 __device__ __noinline__ void row_again(const AttnArgs &a, int64_t q_row, int head, int64_t k_row0, int lim) {
-  constexpr int E = D / 32;
+  constexpr int E = D / 32, kAhead = 8;  // a lane has E neighbouring columns
+  struct alignas(2 * E) Piece {
+    T x[E];
+  };
   const int lane = threadIdx.x & 31, kh = head / (a.n_heads / a.n_kv);
+  const Piece *k = reinterpret_cast<const Piece *>((const T *)a.k + k_row0 * a.k_stride + (int64_t)kh * D) + lane;
+  const Piece *v = reinterpret_cast<const Piece *>((const T *)a.v + k_row0 * a.v_stride + (int64_t)kh * D) + lane;
+  Piece *out = reinterpret_cast<Piece *>((T *)a.out + q_row * a.out_stride + (int64_t)head * D) + lane;
+  Piece r = *out;
   float q[E], o[E], m = -INFINITY, l = 0.f;
+  {
+    const Piece x = reinterpret_cast<const Piece *>((const T *)a.q + q_row * a.q_stride + (int64_t)head * D)[lane];
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    q[e] = to_f32(((const T *)a.q)[q_row * a.q_stride + (int64_t)head * D + lane + 32 * e]);
-    o[e] = 0.f;
+    for (int e = 0; e < E; ++e) q[e] = to_f32(x.x[e]), o[e] = 0.f;
   }
-  for (int j = 0; j < lim; ++j) {
-    const T *k = (const T *)a.k + (k_row0 + j) * a.k_stride + (int64_t)kh * D;
-    const T *v = (const T *)a.v + (k_row0 + j) * a.v_stride + (int64_t)kh * D;
-    float s = 0.f;
+  uint32_t open = 0;  // bit e: column e is not finite
 #pragma unroll
-    for (int e = 0; e < E; ++e) s = fmaf(q[e], to_f32(k[lane + 32 * e]), s);
+  for (int e = 0; e < E; ++e) open |= (uint32_t)!(to_f32(r.x[e]) * 0.f == 0.f) << e;
+  const int64_t k_step = a.k_stride / E, v_step = a.v_stride / E;  // rows lie on 16-byte boundaries
+  for (int j = 0; j < lim; j += kAhead) {
+    float s[kAhead];
+    Piece y[kAhead];
 #pragma unroll
-    for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    s *= a.scale_log2;
-    const float mn = s > m ? s : m;  // a NaN leaves m and makes p a NaN
-    const float f = m == -INFINITY ? 0.f : ex2(m - mn), p = s == -INFINITY ? 0.f : ex2(s - mn);
-    const float old = l * f;
-    l = old + p;
-    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l), w0 = old * inv, w1 = p * inv;
+    for (int u = 0; u < kAhead; ++u) {
+      const int64_t at = min(j + u, lim - 1);
+      const Piece x = k[at * k_step];
+      y[u] = v[at * v_step];
+      s[u] = 0.f;
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = o[e] * w0 + w1 * to_f32(v[lane + 32 * e]);
+      for (int e = 0; e < E; ++e) s[u] = fmaf(q[e], to_f32(x.x[e]), s[u]);
+    }
+#pragma unroll
+    for (int x = 16; x; x >>= 1)
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) s[u] += __shfl_xor_sync(0xffffffffu, s[u], x);
+    float mn = m;
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      s[u] = j + u < lim ? s[u] * a.scale_log2 : -INFINITY;
+      mn = s[u] > mn ? s[u] : mn;  // a NaN leaves m and makes p a NaN
+    }
+    const float old = l * (m == -INFINITY ? 0.f : ex2(m - mn));
+    l = old;
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) s[u] = s[u] == -INFINITY ? 0.f : ex2(s[u] - mn), l += s[u];
+    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+    bool done = true;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      o[e] *= old * inv;
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u)
+        if (j + u < lim) o[e] = fmaf(s[u] * inv, to_f32(y[u].x[e]), o[e]);
+      done = done && (!((open >> e) & 1u) || o[e] != o[e]);
+    }
+    if (__all_sync(0xffffffffu, done)) break;
     m = mn;
   }
 #pragma unroll
   for (int e = 0; e < E; ++e)
-    ((T *)a.out)[q_row * a.out_stride + (int64_t)head * D + lane + 32 * e] = from_f32<T>(o[e]);
+    if ((open >> e) & 1u) r.x[e] = from_f32<T>(o[e]);
+  if (open) *out = r;
 }
 
 template <typename T, int D>
@@ -242,7 +283,7 @@ __global__ void __launch_bounds__(256, Shape<D>::kBlocks)
     for (int i = 0; i < kRing; ++i) ptx::mbar_init(b->full + i, 1), ptx::mbar_init(b->empty + i, 1);
     for (int i = 0; i < 2; ++i)
       ptx::mbar_init(b->s_full + i, 1), ptx::mbar_init(b->p_half + i, 128), ptx::mbar_init(b->p_full + i, 128);
-    ptx::mbar_init(&b->o_full, 1), ptx::mbar_init(&b->done, 1);
+    ptx::mbar_init(&b->o_full, 1), ptx::mbar_init(&b->done, 1), ptx::mbar_init(&b->tail, 1);
     b->dead = 0;
     ptx::mbar_fence_init();
   }
@@ -278,6 +319,10 @@ __global__ void __launch_bounds__(256, Shape<D>::kBlocks)
   const int shift = k_len - q_len;  // query t sees keys 0 .. t + shift
   const int lim_max = work ? max(0, min(q_len, t0 + tile_tok) + shift) : 0;
   const int n_tiles = (lim_max + kKeys - 1) / kKeys;
+  // the second product of the last step goes over `end` keys in steps of 16; of
+  // the values it reads, those from `end` on are seen by no row
+  const int end = lim_max - (n_tiles - 1) * kKeys;
+  const bool cut = lim_max % 16 != 0;
   const int head0 = hb << a.log_group, kh = head0 / (a.n_heads / a.n_kv);
   ptx::tc_fence_before();
   __syncthreads();
@@ -289,9 +334,10 @@ __global__ void __launch_bounds__(256, Shape<D>::kBlocks)
     int st = 0;
     uint32_t ph = 1;  // parity with which an empty stage is waited for (the first round passes)
     bool first_round = true;
-    auto next = [&]() -> uint8_t * {  // null once a wait gave up: no copy is started any more
+    bool tail = false;
+    auto next = [&](uint64_t *bar) -> uint8_t * {  // null once a wait gave up: no copy is started any more
       if (!wait(b, b->empty + st, ph, a.status)) return nullptr;
-      ptx::mbar_expect_tx(b->full + st, kStageBytes);
+      ptx::mbar_expect_tx(bar, kStageBytes);
       return ring + st * kStageBytes;
     };
     auto step = [&]() {
@@ -299,7 +345,7 @@ __global__ void __launch_bounds__(256, Shape<D>::kBlocks)
     };
     auto load_k = [&](int i) {
       for (int h = 0; h < D / 128; ++h) {
-        uint8_t *dst = next();
+        uint8_t *dst = next(b->full + st);
         if (!dst) return;
         for (int d = 0; d < 2; ++d)
           tma_load3(dst + d * kKeys * 128, &mk, 128 * h + 64 * d, kh, k0 + i * kKeys, b->full + st);
@@ -308,10 +354,12 @@ __global__ void __launch_bounds__(256, Shape<D>::kBlocks)
     };
     auto load_v = [&](int i) {
       for (int h = 0; h < kSub; ++h) {
-        uint8_t *dst = next();
+        const bool last = cut && i == n_tiles - 1 && h == end / 64;  // full when warps 2 and 3 say so
+        uint64_t *bar = last ? &b->tail : b->full + st;
+        uint8_t *dst = next(bar);
         if (!dst) return;
-        for (int d = 0; d < D / 64; ++d)
-          tma_load3(dst + d * 8192, &mv, 64 * d, kh, k0 + i * kKeys + h * 64, b->full + st);
+        tail = tail || last;
+        for (int d = 0; d < D / 64; ++d) tma_load3(dst + d * 8192, &mv, 64 * d, kh, k0 + i * kKeys + h * 64, bar);
         step();
       }
     };
@@ -325,6 +373,7 @@ __global__ void __launch_bounds__(256, Shape<D>::kBlocks)
     // after a wait that gave up: what is on its way still lands in this block
     if (*(volatile int *)&b->dead) {
       ptx::mbar_wait_suspend(&b->q_full, 0);
+      if (tail) ptx::mbar_wait_suspend(&b->tail, 0);
       for (int s = 0; s < kRing; ++s)
         if (s < st || !first_round) ptx::mbar_wait_suspend(b->full + s, s < st ? ph ^ 1 : ph);
     }
@@ -338,7 +387,8 @@ __global__ void __launch_bounds__(256, Shape<D>::kBlocks)
     const uint32_t q_lo = (uint32_t)dq, k_lo = (uint32_t)dk, v_lo = (uint32_t)dv, q_hi = (uint32_t)(dq >> 32),
                    k_hi = (uint32_t)(dk >> 32), v_hi = (uint32_t)(dv >> 32);
     // (reductions: the compiler knows their results to be uniform)
-    const uint32_t tm = __reduce_max_sync(0xffffffffu, tmem), steps = __reduce_max_sync(0xffffffffu, (uint32_t)n_tiles);
+    const uint32_t tm = __reduce_max_sync(0xffffffffu, tmem), steps = __reduce_max_sync(0xffffffffu, (uint32_t)n_tiles),
+                   last = __reduce_max_sync(0xffffffffu, (uint32_t)end);
     const uint32_t go = elect_one();
     uint32_t st = 0;  // ring stage of the next K or V tile
     uint32_t ph = 0;
@@ -366,17 +416,18 @@ __global__ void __launch_bounds__(256, Shape<D>::kBlocks)
       }
       umma_done(go, b->s_full + buf);
     };
-    auto outputs = [&](uint32_t buf, bool first, uint32_t turn) {
+    auto outputs = [&](uint32_t buf, bool first, uint32_t turn, uint32_t keys) {
 #pragma unroll
       for (int h = 0; h < kSub; ++h) {
         warp_wait(b->full + st, ph);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
           // the first or second half of the keys' probabilities
-          const int key = 64 * h + 16 * kk;
+          const uint32_t key = 64 * h + 16 * kk;
           if (key % (kKeys / 2) == 0) warp_wait(key == 0 ? b->p_half + buf : b->p_full + buf, turn);
-          umma_ts(go, tm + Sh::kO, tm + kKeys * buf + key / 2, v_lo + st * (kStageBytes >> 4) + kk * (2048 >> 4), v_hi, id_o,
-                  !first || key > 0);
+          if (key < keys)
+            umma_ts(go, tm + Sh::kO, tm + kKeys * buf + key / 2, v_lo + st * (kStageBytes >> 4) + kk * (2048 >> 4), v_hi,
+                    id_o, !first || key > 0);
         }
         umma_done(go, b->empty + st);
         step();
@@ -393,11 +444,27 @@ __global__ void __launch_bounds__(256, Shape<D>::kBlocks)
         if (i > 0) warp_wait(&b->o_full, (i - 1) & 1);
         scores((i + 1) & 1);
       }
-      outputs(i & 1, i == 0, (i >> 1) & 1);
+      outputs(i & 1, i == 0, (i >> 1) & 1, i + 1 < steps ? kKeys : last);
     }
     // (a row may come to its end two products ahead: o_full's parity would not
     // tell the last product from the one before the last)
     umma_done(go, &b->done);
+  } else if ((warp == 2 || warp == 3) && cut) {
+    // ====================== zeros for the values of the last step that no row
+    // of the block sees: a probability of zero times a NaN there would be a NaN
+    // in every row
+    constexpr int kPieces = D / 8, kPass = 64 / kPieces;  // 16-byte pieces of a row; rows at a time
+    // in front of these values lie the keys of all steps and all other values
+    const int st = (D / 128 * n_tiles + kSub * (n_tiles - 1) + end / 64) % kRing;
+    const int piece = (threadIdx.x - 64) % kPieces, r0 = end % 64 + (threadIdx.x - 64) / kPieces, r1 = (end % 64 | 15) + 1;
+    uint8_t *rows = ring + st * kStageBytes + (piece >> 3) * 8192 + ((piece & 7) << 4);
+    wait(b, &b->tail, 0, a.status);
+#pragma unroll
+    for (int i = 0; i < 16; i += kPass)
+      if (r0 + i < r1) *reinterpret_cast<uint4 *>(rows + (r0 + i) * 128) = make_uint4(0u, 0u, 0u, 0u);
+    ptx::fence_proxy_async_smem();
+    asm volatile("bar.sync 1, 64;" ::: "memory");
+    if (threadIdx.x == 64) ptx::mbar_arrive(b->full + st);
   } else if (warp >= 4 && work) {
     // ============================================================== softmax
     const int row0 = 32 * (warp & 3), row = row0 + lane;
@@ -514,7 +581,8 @@ __global__ void __launch_bounds__(256, Shape<D>::kBlocks)
         *reinterpret_cast<uint4 *>((T *)a.out + (int64_t)(q0 + t) * a.out_stride + (int64_t)hd * D + piece * 8) = v;
     }
     ptx::tc_fence_before();
-    uint32_t again = __ballot_sync(0xffffffffu, odd && mine);
+    // (a sum that is NaN comes from a score that counts: the row is NaN)
+    uint32_t again = __ballot_sync(0xffffffffu, odd && mine && l == l);
     __syncwarp();  // the rows are written: an odd one is written again
     while (again) {
       const int src = __ffs(again) - 1;
