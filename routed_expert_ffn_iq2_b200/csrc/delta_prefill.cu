@@ -60,13 +60,17 @@ constexpr int C = 64;  // tokens of a chunk
 // Per (chunk, value head): T and P as two fp16 planes each (rows scaled), the
 // ten 16 x 16 blocks on and under the diagonal (row by row of blocks), a
 // block's rows 32 bytes, their two 16-byte pieces swapped in every other group
-// of four rows (no bank conflicts); then ten per-token factors.
+// of four rows (no bank conflicts); ten per-token factors.  The second plane
+// of P comes last: bf16 outputs are made without it, so it is neither written
+// nor copied for them.
 constexpr int kPlane = 10 * 512;
-enum { kThi, kTlo, kPhi, kPlo, kPlanes };
 // fLast: [0] = exp(c_last); fT, fP: inverse scales of the rows of T and P;
 // fR, fQ, fK, fNk, fNq hold the inverse scales of the keys' and queries' rows
 enum { fBeta, fR, fQ, fK, fAlpha, fNk, fNq, fLast, fT, fP, kFactors };
-constexpr int kHeadBlock = kPlanes * kPlane + kFactors * C * 4;
+constexpr int kThi = 0, kTlo = kPlane, kPhi = 2 * kPlane, kFactorsAt = 3 * kPlane, kPlo = kFactorsAt + kFactors * C * 4;
+constexpr int kHeadBlock = kPlo + kPlane;
+template <typename T>
+constexpr bool kOutLo = !std::is_same<T, __nv_bfloat16>::value;  // outputs from both parts
 
 // Per (chunk, key head): K and Q tiles (NK planes each), rows of 2 DK bytes,
 // pieces swizzled the same way.
@@ -172,7 +176,7 @@ __device__ __forceinline__ void block_product(float (&Y)[2][4], const float (&X)
 struct SameTile {
   __device__ __forceinline__ int operator()(int t) const { return t; }
 };
-template <int NB, typename Get, typename Tile = SameTile>
+template <int NB, bool LO, typename Get, typename Tile = SameTile>
 __device__ __forceinline__ void store_rows(uint8_t *hi, uint8_t *lo, float *f, int block, int n, int lane, Get get,
                                            Tile tile = Tile()) {
   const int r = lane >> 2, c = lane & 3;
@@ -198,8 +202,8 @@ __device__ __forceinline__ void store_rows(uint8_t *hi, uint8_t *lo, float *f, i
     split_f16(v[0] * s0, v[1] * s0, h0, l0);
     split_f16(v[2] * s1, v[3] * s1, h1, l1);
     const uint32_t o0 = tp_off(16 * block + r, tile(t)) + 4 * c, o1 = tp_off(16 * block + r + 8, tile(t)) + 4 * c;
-    *reinterpret_cast<uint32_t *>(hi + o0) = h0, *reinterpret_cast<uint32_t *>(lo + o0) = l0;
-    *reinterpret_cast<uint32_t *>(hi + o1) = h1, *reinterpret_cast<uint32_t *>(lo + o1) = l1;
+    *reinterpret_cast<uint32_t *>(hi + o0) = h0, *reinterpret_cast<uint32_t *>(hi + o1) = h1;
+    if (LO) *reinterpret_cast<uint32_t *>(lo + o0) = l0, *reinterpret_cast<uint32_t *>(lo + o1) = l1;
   }
 }
 
@@ -360,8 +364,7 @@ __global__ void __launch_bounds__(256, 2) delta_prep_kernel(const DeltaArgs a, c
     // 2 to the difference of two sums: what is rounded is the difference
     auto decay = [&](float2 x, float2 y) { return ex2((x.x - y.x) + (x.y - y.y)); };
     if (have) {
-      float *f = reinterpret_cast<float *>(a.ws + w.head + ((size_t)slot * a.n_v + head) * kHeadBlock +
-                                           kPlanes * kPlane);
+      float *f = reinterpret_cast<float *>(a.ws + w.head + ((size_t)slot * a.n_v + head) * kHeadBlock + kFactorsAt);
       const float2 none = make_float2(0.f, 0.f), mine = sc[half][tok], last = sc[half][C - 1];
       const float gamma = decay(mine, none);
       f[fBeta * C + tok] = b;
@@ -405,9 +408,8 @@ __global__ void __launch_bounds__(256, 2) delta_prep_kernel(const DeltaArgs a, c
         }
       }
       if (group) {
-        store_rows<8>(blk + kPhi * kPlane, blk + kPlo * kPlane,
-                      reinterpret_cast<float *>(blk + kPlanes * kPlane) + fP * C, role, 2 * role + 2, lane,
-                      [&](int t) { return v[t]; });
+        store_rows<8, kOutLo<T>>(blk + kPhi, blk + kPlo, reinterpret_cast<float *>(blk + kFactorsAt) + fP * C, role,
+                                 2 * role + 2, lane, [&](int t) { return v[t]; });
       } else {
 #pragma unroll
         for (int t = 0; t < 8; ++t) {
@@ -475,10 +477,9 @@ __global__ void __launch_bounds__(256, 2) delta_prep_kernel(const DeltaArgs a, c
       block_product(X[d], Y, td[q][j], kPitchT, lane);
     }
     // columns 16 (role - d) + 8 nb of the row: tile 2 (role - d) + nb
-    store_rows<8>(blk + kThi * kPlane, blk + kTlo * kPlane, reinterpret_cast<float *>(blk + kPlanes * kPlane) + fT * C,
-                  role, 2 * role + 2, lane, [&](int t) { return X[t >> 1][t & 1]; }, [&](int t) {
-                    return 2 * (role - (t >> 1)) + (t & 1);
-                  });
+    store_rows<8, true>(blk + kThi, blk + kTlo, reinterpret_cast<float *>(blk + kFactorsAt) + fT * C, role, 2 * role + 2,
+                        lane, [&](int t) { return X[t >> 1][t & 1]; },
+                        [&](int t) { return 2 * (role - (t >> 1)) + (t & 1); });
   }
 }
 
@@ -503,8 +504,9 @@ struct ChainBars {
 // The plan of a chain block's shared memory.
 template <typename T, int NK, int DK>
 struct Chain {
-  static constexpr bool kLo = !std::is_same<T, __nv_bfloat16>::value;  // outputs from both parts
-  static constexpr int kStage = kq_bytes<NK, DK>() + kHeadBlock;
+  static constexpr bool kLo = kOutLo<T>;
+  static constexpr int kHead = kLo ? kHeadBlock : kPlo;  // bytes of a head's block that are used
+  static constexpr int kStage = kq_bytes<NK, DK>() + kHead;
   static constexpr int kV = C * 8 * (int)sizeof(T);  // a chain warp's values of a chunk
   static constexpr int kRest = 2 * kChains * kV + kChains * (int)sizeof(Handoff<kLo>) + (int)sizeof(ChainBars<3>);
   static constexpr int kStages = 3 * kStage + kRest <= 227 * 1024 ? 3 : 2;
@@ -539,28 +541,29 @@ __device__ __forceinline__ void load_rows(uint32_t tile, int ks, int lane, uint3
   for (int t = 0; t < 4; ++t)
     ldsm4(tile + kq_off<DK>(16 * t + (lane & 15), 2 * ks + (lane >> 4)), a[t][0], a[t][1], a[t][2], a[t][3]);
 }
-// The lower triangle's blocks (two planes) of 16 columns.
+// The lower triangle's blocks (of a plane, and of the one `to_lo` bytes on) of
+// 16 columns.
 template <bool LO>
-__device__ __forceinline__ void load_triangle(uint32_t planes, int ks, int lane, uint32_t (&p)[4][4], uint32_t (&q)[4][4]) {
+__device__ __forceinline__ void load_triangle(uint32_t planes, uint32_t to_lo, int ks, int lane, uint32_t (&p)[4][4], uint32_t (&q)[4][4]) {
 #pragma unroll
   for (int t = 0; t < 4; ++t)
     if (t >= ks) {
       const uint32_t off = planes + tp_off(16 * t + (lane & 15), 2 * ks + (lane >> 4));
       ldsm4(off, p[t][0], p[t][1], p[t][2], p[t][3]);
-      if (LO) ldsm4(off + kPlane, q[t][0], q[t][1], q[t][2], q[t][3]);
+      if (LO) ldsm4(off + to_lo, q[t][0], q[t][1], q[t][2], q[t][3]);
     }
 }
 // acc = L B: the triangle times the B operands of 64 rows; p[0] and q[0] hold
 // its first 16 columns, the next ones are read while products run.
 template <bool LO>
-__device__ __forceinline__ void triangle(float (&acc)[4][4], uint32_t planes, const uint32_t (&h)[4][2],
-                                         const uint32_t (&l)[4][2], int lane, uint32_t (&p)[2][4][4],
+__device__ __forceinline__ void triangle(float (&acc)[4][4], uint32_t planes, uint32_t to_lo,
+                                         const uint32_t (&h)[4][2], const uint32_t (&l)[4][2], int lane, uint32_t (&p)[2][4][4],
                                          uint32_t (&q)[2][4][4]) {
   float more[4][4];
   zero(acc), zero(more);
 #pragma unroll
   for (int ks = 0; ks < 4; ++ks) {
-    if (ks < 3) load_triangle<LO>(planes, ks + 1, lane, p[(ks + 1) & 1], q[(ks + 1) & 1]);
+    if (ks < 3) load_triangle<LO>(planes, to_lo, ks + 1, lane, p[(ks + 1) & 1], q[(ks + 1) & 1]);
 #pragma unroll
     for (int t = ks; t < 4; ++t) mma_f16(acc[t], p[ks & 1][t], h[ks][0], h[ks][1]);
     if (LO) {
@@ -662,7 +665,7 @@ __global__ void __launch_bounds__(32 * (2 * kChains + 1), 1) delta_chain_kernel(
         ptx::bulk_g2s(dst, a.ws + w.kq + ((size_t)(slot0 + i) * a.n_k + kh) * kq_bytes<NK, DK>(), kq_bytes<NK, DK>(),
                       bars->full + st);
         ptx::bulk_g2s(dst + kq_bytes<NK, DK>(), a.ws + w.head + ((size_t)(slot0 + i) * a.n_v + head) * kHeadBlock,
-                      kHeadBlock, bars->full + st);
+                      Plan::kHead, bars->full + st);
       }
     return;
   }
@@ -696,8 +699,8 @@ __global__ void __launch_bounds__(32 * (2 * kChains + 1), 1) delta_chain_kernel(
     for (int i = 0; i < n_chunks; ++i) {
       const int st = i % kStages, n = min(C, sp.len - i * C);
       const uint32_t sQ = ptx::smem_u32(smem + st * kStage) + NK * kTile;
-      const uint32_t sP = sQ + NK * kTile + kPhi * kPlane;
-      const float *f = reinterpret_cast<const float *>(smem + st * kStage + kq_bytes<NK, DK>() + kPlanes * kPlane);
+      const uint32_t sP = sQ + NK * kTile + kPhi;
+      const float *f = reinterpret_cast<const float *>(smem + st * kStage + kq_bytes<NK, DK>() + kFactorsAt);
       if (!wait(bars->full + st, (i / kStages) & 1) || !wait(bars->s_ready + me, i & 1)) break;
       float O[4][4];
       zero(O);
@@ -737,14 +740,14 @@ __global__ void __launch_bounds__(32 * (2 * kChains + 1), 1) delta_chain_kernel(
       arrive(bars->d_taken + me);
       if (!walk) {
         uint32_t p[2][4][4], q[2][4][4];
-        load_triangle<kLo>(sP, 0, lane, p[0], q[0]);
+        load_triangle<kLo>(sP, kPlo - kPhi, 0, lane, p[0], q[0]);
         col_max(m0, m1);
         float i0, i1;
         const float s0 = scale_f16(m0, i0), s1 = scale_f16(m1, i1);
         uint32_t h[4][2], l[4][2];
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) split_tile(D[ks], s0, s1, h[ks], l[ks]);
-        triangle<kLo>(D, sP, h, l, lane, p, q);
+        triangle<kLo>(D, sP, kPlo - kPhi, h, l, lane, p, q);
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
@@ -796,7 +799,7 @@ __global__ void __launch_bounds__(32 * (2 * kChains + 1), 1) delta_chain_kernel(
   for (int i = 0; i < n_chunks; ++i) {
     const int st = i % kStages, n = min(C, sp.len - i * C);
     const uint32_t sK = ptx::smem_u32(smem + st * kStage), sT = sK + kq_bytes<NK, DK>();
-    const float *f = reinterpret_cast<const float *>(smem + st * kStage + kq_bytes<NK, DK>() + kPlanes * kPlane);
+    const float *f = reinterpret_cast<const float *>(smem + st * kStage + kq_bytes<NK, DK>() + kFactorsAt);
     const T *vt = reinterpret_cast<const T *>(vbuf + (2 * me + (i & 1)) * Plan::kV);
     const uint32_t full = test(bars->full + st, (i / kStages) & 1);
     const uint32_t s_free = i == 0 || test(bars->s_taken + me, (i - 1) & 1);
@@ -856,7 +859,7 @@ __global__ void __launch_bounds__(32 * (2 * kChains + 1), 1) delta_chain_kernel(
     if (r == 0) ho.scale[c] = make_float2(u0, u1);
     arrive(bars->s_ready + me);
     uint32_t tp[2][4][4], tq[2][4][4];
-    load_triangle<true>(sT, 0, lane, tp[0], tq[0]);
+    load_triangle<true>(sT, kTlo - kThi, 0, lane, tp[0], tq[0]);
     // ---- beta V - beta exp(c) K S
     float m0 = 0.f, m1 = 0.f;
 #pragma unroll
@@ -882,7 +885,7 @@ __global__ void __launch_bounds__(32 * (2 * kChains + 1), 1) delta_chain_kernel(
     float ft[8], fk[8];
 #pragma unroll
     for (int m = 0; m < 8; ++m) ft[m] = f[fT * C + 8 * m + r], fk[m] = f[fK * C + 8 * m + r];
-    triangle<true>(D, sT, h, l, lane, tp, tq);
+    triangle<true>(D, sT, kTlo - kThi, h, l, lane, tp, tq);
     // K^T of 16 tokens
     uint32_t kt[2][NT][4];
     auto load_keys = [&](int step) {  // step: tokens 16 (step / NK) .., plane step % NK

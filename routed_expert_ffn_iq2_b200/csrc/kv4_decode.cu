@@ -861,7 +861,7 @@ extern "C" int redlite_kv4_decode(int32_t dtype, const void *q, int64_t q_stride
   if (!stride_ok(q_stride, row, dtype) || !stride_ok(out_stride, row, dtype)) return REDLITE_EINVAL;
   if ((int64_t)n_seqs * n_heads >= ((int64_t)1 << 31) - 1) return REDLITE_EUNSUPPORTED;
   if (workspace_bytes < redlite_kv4_decode_workspace_bytes(n_seqs, n_heads, n_kv_heads, head_dim)) return REDLITE_ENOMEM;
-  const int sms = sm_count();
+  const int sms = device_sms();
   if (sms <= 0) return REDLITE_ECUDA;
   DecArgs a;
   a.q = q, a.out = out, a.q_stride = q_stride, a.out_stride = out_stride;

@@ -18,18 +18,6 @@ inline bool stride_ok(int64_t stride, int64_t row, int32_t dtype) {
   return stride >= row && stride <= ((int64_t)1 << 40) && (stride * dtype_bytes(dtype)) % 16 == 0;
 }
 
-// Multiprocessors of the current device (queried once per device; a device
-// past the table is asked every time).
-inline int sm_count() {
-  static int cached[64];
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-  if (dev >= 0 && dev < 64 && cached[dev]) return cached[dev];
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-  if (dev >= 0 && dev < 64) cached[dev] = n;
-  return n;
-}
-
 // Launch a kernel that may be set up while the one in front of it in the
 // stream still runs: the kernel calls after_predecessor() first, on every way
 // out too, and touches nothing before (so whatever that kernel is, its results
@@ -108,12 +96,6 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 }
 __device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
-// x = hi + lo with hi, lo in bf16: what is left out is at most 2^-17 of x.
-__device__ __forceinline__ void split_bf16(float a, float b, uint32_t &hi, uint32_t &lo) {
-  hi = pack_bf16(a, b);
-  lo = pack_bf16(a - bf16_lo(hi), b - bf16_hi(hi));
-}
-
 // x = hi + lo with hi, lo in fp16, for values below 2^15: what is left out is
 // at most 2^-23 of x, or 2^-25 where x is small (fp16's smallest step).
 __device__ __forceinline__ void split_f16(float a, float b, uint32_t &hi, uint32_t &lo) {
