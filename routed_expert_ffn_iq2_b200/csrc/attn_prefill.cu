@@ -33,10 +33,12 @@
 // the other block's steps where there are two (one block of two row tiles, a
 // softmax group each: 82 us for the ragged batch below).
 //
-// Measured (one B200): 16384 tokens, 16 heads on 2 of 256, bf16: 1.62 to 1.73 ms,
-// 1.27 to 1.36 PFLOP/s (a long library product: 1.39); five ragged fp16 prompts,
-// 3957 tokens of 32 heads on 8 of 128: 68 to 72 us, 666 to 700 TFLOP/s; three of 43 tokens
-// together 8.1 us.  Tried without gain: two threads a row in the softmax,
+// Measured (one B200): 16384 tokens, 16 heads on 2 of 256, bf16: 1.71 to 1.73 ms,
+// 1.27 to 1.29 PFLOP/s (a long library product: 1.39); five ragged fp16 prompts,
+// 3957 tokens of 32 heads on 8 of 128: 72 us, 660 TFLOP/s; three of 43 tokens
+// together 7.7 us.  Rounding p costs: error against 64 bits 2.2e-3 of the output
+// for the long bf16 prompt (1.6e-3 is the output's own rounding), 2.6e-4 for the
+// fp16 batch (2.1e-4).  Tried without gain: two threads a row in the softmax,
 // polynomials for a part of the exponentials, probabilities handed over in one
 // piece, tiles of all sequences by their keys instead of sequence by sequence.
 //
@@ -45,9 +47,11 @@
 // sequence, or later tokens) the last product leaves out all it can, and the
 // values of the up to 15 others are set to zero in shared memory (with NaN
 // behind 8189 keys, 512 queries of 16 heads took 142 ms without, as every row
-// of the last tile was computed again).  Among a block's own tokens,
-// and where a sum over values past 10^36 leaves fp32, the columns of a row that
-// are not finite are computed again by its warp from the keys it sees alone.
+// of the last tile was computed again).  Among a block's own tokens, and where
+// a sum over values past 10^36 leaves fp32, the columns of a row that are not
+// finite are computed again by its warp from the keys it sees alone (a NaN in
+// the last of 8192 values: 35 ms, 1 ms for each of a warp's 32 rows; one among
+// the first keys: nothing that shows).
 #include <cuda.h>
 
 #include <type_traits>

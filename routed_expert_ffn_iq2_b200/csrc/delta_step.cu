@@ -11,8 +11,8 @@
 // needs no second one.  A block owns 32 columns of one head's state (rows of
 // 128 bytes, 16 KB): a single sequence of 32 heads spreads over 128 blocks,
 // and in large batches some ten blocks per multiprocessor keep 16 KB each in
-// flight.  All sums are fp32.  Measured: 200 sequences of 32 heads 133 us, 6.3
-// TB/s (97% of the copy rate); one sequence 3.1 us.
+// flight.  All sums are fp32.  Measured: 200 sequences of 32 heads 133 to 138
+// us, 6.1 to 6.3 TB/s (94 to 97% of the copy rate); one sequence 3.1 us.
 #include "delta.cuh"
 
 namespace redlite {

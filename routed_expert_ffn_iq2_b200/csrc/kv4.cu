@@ -14,7 +14,7 @@
 // quantiser keeps off the conversion and 64-bit units.  Measured: 8096 tokens
 // of two heads of 256, bf16 in and fp32 out, 16 us in and 12 us out alone, 23 us
 // for both in a row (their bytes take 9 us; 25 us with 32-bit values stored as
-// each thread holds them); 16 tokens 5.6 us for both.  With
+// each thread holds them); 16 tokens 5.8 us for both.  With
 // 64-bit places and quotients: 40 us and 15 us.
 #include "kv4.cuh"
 

@@ -26,8 +26,8 @@
 //               p <= 2^15 / max(1, |d|) for the largest |d| met so far.  Small
 //               steps count as 2^lift times themselves, so that p d stays above
 //               fp16's subnormal numbers: what falls below them all the same is
-//               off by 2^-22 of the largest p d at most (without: by 2^-25 of a p
-//               of 2^6 to 2^14, 2^-9 of the output where values are 1e-6)
+//               off by 2^-22 of the largest p d at most (without: by 2^-10 of it
+//               for steps of 2^-21, 1.8 times the bound of 30,000 such tokens)
 //   fp32        the query in three bf16 parts (exact); 16 d p and p in three.
 //               Codes are centred in the scores too: q . K_t = sum_g 16 d_tg (q_g
 //               . (code - 8) / 16) + (m_tg + 8 d_tg) sum(q_g), so that no sum is
@@ -44,12 +44,16 @@
 // adds up in a fixed order: no atomics, nothing kept from call to call.
 //
 // Measured (one B200, floor at 6550 GB/s in brackets): 16 contexts of 49k to
-// 66k tokens, 32 heads on 8 of 128, fp16: 320 us, 3.7 TB/s [180 us]; 64 ragged
-// contexts up to 8k, 16 heads on 2 of 256, bf16: 60 us [24 us]; one of 700
-// tokens, fp32: 12 us.  What bounds the long case is instructions: 467 a tile
-// of 16 tokens of 128, half of them on the integer units (which take one every
-// other cycle), with 16 warps a multiprocessor (128 registers, what the
-// accumulators leave).
+// 66k tokens, 32 heads on 8 of 128, fp16: 331 us, 3.5 TB/s [178 us]; 64 ragged
+// contexts up to 8k, 16 heads on 2 of 256, bf16: 59 us [24 us]; one of 700
+// tokens, fp32: 12 us.  No unit is saturated: integer units 53% of their rate,
+// DRAM 34%, tensor cores 17%, 2.1 to 2.3 instructions a cycle.  With four warps
+// a scheduler (128 registers, what the accumulators leave) latency shows: of a
+// warp's 6 cycles an instruction it waits 1.4 for the one before it, 0.8 for
+// the integer units and 0.4 to 0.8 each for shared memory, tiles and the other
+// warps.  Heads of 256 spill some of their registers (200 to 350 bytes).  More
+// than 8 query heads per key/value head go in blocks of 8, each of which reads
+// and converts the cache for itself: 9 to 16 heads have twice the floor.
 #include "kv4.cuh"
 
 namespace redlite {
