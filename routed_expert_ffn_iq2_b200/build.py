@@ -16,7 +16,6 @@ CSRC = os.path.join(PKG, "csrc")
 OBJ = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libredlite_moe.so")
 MARSHAL = os.path.join(PKG, "_marshal.so")
-MARSHAL_ABI = os.path.join(OBJ, "_marshal.abi")  # what the marshaller was built against
 
 CXX = os.environ.get("CXX", "g++")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
@@ -52,10 +51,10 @@ def marshal_abi() -> str:
 
 
 def marshal_abi_matches() -> bool:
-    """Whether _marshal.so was built against this Python and torch (and its last build went through)."""
+    """Whether _marshal.so was built against this Python and torch (the binary holds what it was built against)."""
     try:
-        with open(MARSHAL_ABI) as f:
-            return f.read() == marshal_abi()
+        with open(MARSHAL, "rb") as f:
+            return f"redlite_marshal_abi:{marshal_abi()};".encode() in f.read()
     except OSError:
         return False
 
@@ -68,9 +67,8 @@ def build_marshal(force: bool = False) -> str:
         return MARSHAL
     import torch
 
-    os.makedirs(OBJ, exist_ok=True)
-    if os.path.exists(MARSHAL_ABI):
-        os.remove(MARSHAL_ABI)  # until the build below has gone through
+    if os.path.exists(MARSHAL):
+        os.remove(MARSHAL)  # it is out of date, whether or not the build below goes through
     t = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(NVCC))
     inc = [os.path.join(ROOT, "include"), os.path.join(t, "include"),
@@ -78,15 +76,13 @@ def build_marshal(force: bool = False) -> str:
            sysconfig.get_paths()["include"]]
     tmp = MARSHAL + ".tmp"
     r = subprocess.run([CXX, "-O2", "-std=c++17", "-fPIC", "-shared", *[a for i in inc for a in ("-isystem", i)],
-                        f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", src, "-o", tmp,
+                        f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DREDLITE_MARSHAL_ABI="{marshal_abi()}"', src, "-o", tmp,
                         "-L", PKG, "-l:libredlite_moe.so", "-Wl,-rpath,$ORIGIN", "-L", os.path.join(t, "lib"),
                         "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"],
                        stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
     if r.returncode != 0:
         raise RuntimeError("marshal.cpp failed:\n" + r.stdout.decode(errors="replace"))
     os.replace(tmp, MARSHAL)
-    with open(MARSHAL_ABI, "w") as f:
-        f.write(marshal_abi())
     return MARSHAL
 
 
@@ -95,7 +91,7 @@ def _try_marshal(force: bool = False) -> None:
     Python calls alone (they raise), not the C ABI nor the routed layer."""
     try:
         build_marshal(force)
-    except (OSError, RuntimeError) as e:
+    except (ImportError, OSError, RuntimeError) as e:
         warnings.warn(f"the token mixers' Python calls are not available: {e}")
 
 

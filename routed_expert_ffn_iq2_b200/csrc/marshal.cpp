@@ -12,6 +12,11 @@
 
 #include "redlite_moe.h"
 
+// What this file was built against (the build gives it); read from the binary
+// before it is loaded.
+extern "C" __attribute__((used, visibility("default"))) const char redlite_marshal_abi[];
+const char redlite_marshal_abi[] = "redlite_marshal_abi:" REDLITE_MARSHAL_ABI ";";
+
 namespace {
 
 struct Bad {};      // arguments that do not fit together: REDLITE_EINVAL

@@ -11,7 +11,6 @@ def B(tmp_path, monkeypatch):
 
     build.build()
     monkeypatch.setattr(build, "MARSHAL", str(tmp_path / "_marshal.so"))
-    monkeypatch.setattr(build, "MARSHAL_ABI", str(tmp_path / "_marshal.abi"), raising=False)
     return build
 
 
@@ -42,8 +41,9 @@ def test_a_binary_of_another_torch_is_built_again(B, native, monkeypatch):
 
     def compiler(cmd, **kw):
         calls.append(cmd)
+        abi = next(a for a in cmd if a.startswith("-DREDLITE_MARSHAL_ABI="))
         with open(cmd[cmd.index("-o") + 1], "w") as f:
-            f.write("binary")
+            f.write("binary redlite_marshal_abi:" + abi.split("=", 1)[1].strip('"') + "; binary")
         return type("R", (), {"returncode": 0, "stdout": b""})()
 
     monkeypatch.setattr(B.subprocess, "run", compiler)
@@ -66,3 +66,19 @@ def test_a_binary_of_another_torch_is_built_again(B, native, monkeypatch):
         B.build()
     monkeypatch.setattr(torch, "__version__", "9.9")
     assert not B.marshal_abi_matches()
+    assert not os.path.exists(B.MARSHAL)
+
+
+def test_the_library_is_built_without_torch(B, monkeypatch):
+    import sys
+
+    monkeypatch.setitem(sys.modules, "torch", None)
+    with pytest.warns(UserWarning, match="token mixers"):
+        assert B.build() == B.LIB
+
+
+def test_the_binary_tells_what_it_was_built_against():
+    from routed_expert_ffn_iq2_b200 import build
+
+    build.build()
+    assert build.marshal_abi_matches()
