@@ -373,8 +373,9 @@ int redlite_proj_gemv(int32_t qtype, const void *W, int64_t rows, int64_t k, con
  *   out[i, h] = sum_j softmax_j(scale * q[i, h] . k[j, kh]) v[j, kh]
  * kh = h / (n_heads / n_kv_heads); query i of sequence s (nq queries, nk
  * keys) sees keys 0 .. i + nk - nq of that sequence (the last query sees
- * all); a query that sees none gives zeros.  What a masked place holds (NaN
- * and infinities included) has no effect.
+ * all); a query that sees none gives zeros, and so does one whose scores are
+ * all -infinity (a key with that score has no weight).  What a masked place
+ * holds (NaN and infinities included) has no effect.
  *   dtype       REDLITE_T_BF16 or REDLITE_T_F16 (else EUNSUPPORTED: the
  *               products run on the tensor cores in the inputs' own type)
  *   q, out      device [n_q rows, n_heads * head_dim]

@@ -85,6 +85,26 @@ def test_one_bad_value_decides_its_column_alone(P, t, D, val):
 
 
 @gpu
+@pytest.mark.parametrize("t", TA.TYPES)
+@pytest.mark.parametrize("D", [128, 256])
+def test_a_score_of_minus_infinity_has_no_weight(P, t, D):
+    """An infinite key element against a negative query element: as if the key were not there; zeros where all are."""
+    rng = np.random.default_rng(D)
+    q, k, v = TA._inputs(rng, t, 3, 150, 4, 2, D)
+    q[:, :, 0] = -1
+    keep = np.ones(150, bool)
+    keep[[0, 70, 149]] = False
+    k[torch.tensor(~keep).cuda(), :, 0] = float("inf")
+    out = torch.empty_like(q)
+    assert P.redlite_attn_prefill(q[2:], k, v, R.cu([1]), R.cu([150]), out[2:], 0.1) == P.REDLITE_OK
+    ref, lim = TA._reference(TA._host(q)[2:], TA._host(k)[keep], TA._host(v)[keep], [1], [147], 0.1, t)
+    TA._check(out[2:], ref, lim)
+    k[:, :, 0] = float("inf")
+    assert P.redlite_attn_prefill(q, k, v, R.cu([3]), R.cu([150]), out, 0.1) == P.REDLITE_OK
+    assert bool((out == 0).all())
+
+
+@gpu
 @pytest.mark.parametrize("where", ["behind", "key", "first value", "all values"])
 def test_time_with_values_that_are_not_finite(P, where):
     """A prompt over a long context: not an order of magnitude slower for a NaN behind it, in a key or in its values."""
