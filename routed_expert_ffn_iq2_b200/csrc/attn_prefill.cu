@@ -33,7 +33,7 @@
 // the other block's steps where there are two (one block of two row tiles, a
 // softmax group each: 82 us for the ragged batch below).
 //
-// Measured (one B200): 16384 tokens, 16 heads on 2 of 256, bf16: 1.71 to 1.73 ms,
+// Measured (one B200): 16384 tokens, 16 heads on 2 of 256, bf16: 1.70 to 1.73 ms,
 // 1.27 to 1.29 PFLOP/s (a long library product: 1.39); five ragged fp16 prompts,
 // 3957 tokens of 32 heads on 8 of 128: 72 us, 660 TFLOP/s; three of 43 tokens
 // together 7.7 us.  Rounding p costs: error against 64 bits 2.2e-3 of the output
